@@ -12,6 +12,7 @@ allocate outputs with torch and call them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -30,6 +31,8 @@ FP8_OK = 0
 FP8_ERR_INVALID_ARG, FP8_ERR_UNSUPPORTED, FP8_ERR_MISALIGNED = -1, -2, -3
 FP8_ERR_CUDA, FP8_ERR_DEVICE_TIMEOUT, FP8_ERR_WORKSPACE = -4, -5, -6
 FP8_ERR_TOO_LARGE = -7
+FP8_RAGGED_M, FP8_RAGGED_K = 0, 1
+FP8_MAX_GROUPS, FP8_MAX_INT8_K = 1024, 131071
 FP8_MAX = {FP8_E4M3: 448.0, FP8_E5M2: 57344.0}
 
 
@@ -98,6 +101,28 @@ class LinearBwdArgs(ctypes.Structure):
                 ("workspace", _P), ("workspace_bytes", _SZ)]
 
 
+class Groups(ctypes.Structure):
+    _fields_ = [("groups", _I64), ("offsets", _P), ("offsets_64", _I),
+                ("stride_b", _I64), ("stride_d", _I64), ("scale_b_step", _I)]
+
+
+class MmInt8Args(ctypes.Structure):
+    _fields_ = [("m", _I64), ("n", _I64), ("k", _I64),
+                ("a", _P), ("lda", _I64), ("b", _P), ("ldb", _I64),
+                ("scale_a", _P), ("scale_b", _P),
+                ("bias", _P), ("bias_dtype", _I),
+                ("d", _P), ("d_dtype", _I), ("ldd", _I64)]
+
+
+class LinearInt8Args(ctypes.Structure):
+    _fields_ = [("M", _I64), ("N", _I64), ("K", _I64),
+                ("x", _P), ("x_dtype", _I), ("ldx", _I64),
+                ("w8", _P), ("ldw8", _I64), ("sw", _P),
+                ("bias", _P), ("bias_dtype", _I),
+                ("x8", _P), ("ldx8", _I64), ("sx_out", _P),
+                ("y", _P), ("y_dtype", _I), ("ldy", _I64)]
+
+
 _SIGS = {
     "fp8_ring_bytes": (_SZ, [_I]),
     "fp8_ring_init": (_I, [_P, _I, _P]),
@@ -109,6 +134,12 @@ _SIGS = {
     "fp8_mm_plan": (_I, [ctypes.POINTER(MmArgs), ctypes.POINTER(MmArgs), _I, ctypes.POINTER(MmPlanInfo)]),
     "fp8_mm_pair": (_I, [ctypes.POINTER(MmArgs), ctypes.POINTER(MmArgs), _P]),
     "fp8_mm_batched": (_I, [ctypes.POINTER(MmArgs), _I64, _I64, _I64, _I64, _P]),
+    "fp8_mm_grouped": (_I, [ctypes.POINTER(MmArgs), _I, ctypes.POINTER(Groups), _P]),
+    "fp8_quantize_int8": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "fp8_mm_int8": (_I, [ctypes.POINTER(MmInt8Args), _P]),
+    "fp8_linear_grouped_forward": (_I, [ctypes.POINTER(LinearFwdArgs), ctypes.POINTER(Groups), _P]),
+    "fp8_linear_grouped_backward": (_I, [ctypes.POINTER(LinearBwdArgs), ctypes.POINTER(Groups), _P]),
+    "fp8_linear_int8_forward": (_I, [ctypes.POINTER(LinearInt8Args), _P]),
     "fp8_mm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "fp8_quantize_ex": (_I, [ctypes.POINTER(QuantizeArgs), _I, _P]),
     "fp8_ring_finalize": (_I, [_P, _I, _I, _P, _P]),
@@ -244,6 +275,35 @@ def fp8_mm_batched(a: MmArgs, batch: int, stride_a: int, stride_b: int, stride_d
     """batch GEMMs of a's shape; element strides between batches (0 shares an operand)."""
     _check(_lib.fp8_mm_batched(ctypes.byref(a), batch, stride_a, stride_b, stride_d, _stream(device)),
            "fp8_mm_batched")
+
+
+def fp8_mm_grouped(a: MmArgs, ragged: int, groups: Groups, device=None) -> None:
+    """Products grouped by expert: FP8_RAGGED_M (rows of A and D) or FP8_RAGGED_K (the contraction)."""
+    _check(_lib.fp8_mm_grouped(ctypes.byref(a), ragged, ctypes.byref(groups), _stream(device)), "fp8_mm_grouped")
+
+
+def fp8_quantize_int8(x: torch.Tensor, out: torch.Tensor, scale: torch.Tensor) -> None:
+    rows, cols = x.shape
+    _check(_lib.fp8_quantize_int8(_ptr(x), _dtype_code(x), rows, cols, _ld(x), _ptr(out), _ld(out), _ptr(scale),
+                                  _stream(x.device)), "fp8_quantize_int8")
+
+
+def fp8_mm_int8(a: MmInt8Args, device=None) -> None:
+    _check(_lib.fp8_mm_int8(ctypes.byref(a), _stream(device)), "fp8_mm_int8")
+
+
+def fp8_linear_grouped_forward(args: LinearFwdArgs, groups: Groups, device=None) -> None:
+    _check(_lib.fp8_linear_grouped_forward(ctypes.byref(args), ctypes.byref(groups), _stream(device)),
+           "fp8_linear_grouped_forward")
+
+
+def fp8_linear_grouped_backward(args: LinearBwdArgs, groups: Groups, device=None) -> None:
+    _check(_lib.fp8_linear_grouped_backward(ctypes.byref(args), ctypes.byref(groups), _stream(device)),
+           "fp8_linear_grouped_backward")
+
+
+def fp8_linear_int8_forward(args: LinearInt8Args, device=None) -> None:
+    _check(_lib.fp8_linear_int8_forward(ctypes.byref(args), _stream(device)), "fp8_linear_int8_forward")
 
 
 def fp8_mm(m, n, k, a, fmt_a, a_major, lda, b, fmt_b, b_major, ldb, scale_a, scale_b, d, ldd,
@@ -468,3 +528,214 @@ def linear_backward(g, fwd: ForwardResult, ring_g: ScaleRing | None, fmt_g=FP8_E
         _ptr(workspace), (workspace.numel() * workspace.element_size()) if workspace is not None else 0)
     fp8_linear_backward(args, dev)
     return BackwardResult(dx, dw, dbias, g8, sc[0:1], sc[1:2])
+
+
+# --------------------------------------------------------------------------- grouped and int8
+
+_FP8_CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def _on_device(dev: torch.device, *tensors: torch.Tensor | None):
+    """The operands' device made current for the call (a no-op on the current
+    one); every tensor has to live there."""
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    return torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else contextlib.nullcontext()
+
+
+def _groups(offsets: torch.Tensor, stride_b: int = 0, stride_d: int = 0, scale_b_step: int = 0) -> Groups:
+    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.stride(0) != 1 or \
+            offsets.dtype not in (torch.int32, torch.int64):
+        raise ValueError("offsets: a contiguous int32 or int64 vector of groups + 1 row offsets")
+    return Groups(offsets.numel() - 1, offsets.data_ptr(), int(offsets.dtype == torch.int64), stride_b, stride_d,
+                  scale_b_step)
+
+
+def _expert_matrix(w: torch.Tensor, groups: int, what: str) -> int:
+    """Row stride of a [groups, rows, cols] tensor whose matrices follow one another row by row."""
+    if w.dim() != 3 or w.shape[0] != groups:
+        raise ValueError(f"{what}: expected [groups, rows, columns] with {groups} groups, got {tuple(w.shape)}")
+    if w.shape[2] > 1 and w.stride(2) != 1:
+        raise ValueError(f"{what}: the last dimension has to be contiguous")
+    ld = w.stride(1)
+    if w.shape[0] > 1 and w.stride(0) != w.shape[1] * ld:
+        raise ValueError(f"{what}: the groups' matrices have to follow one another (stride {w.shape[1] * ld}, "
+                         f"got {w.stride(0)})")
+    return ld
+
+
+def _scale_step(scale: torch.Tensor, groups: int, what: str) -> int:
+    if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() not in (1, groups):
+        raise ValueError(f"{what}: a contiguous fp32 tensor of 1 or {groups} scales")
+    return int(scale.numel() != 1)
+
+
+def _out(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev, what: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def fp8_alloc_experts(groups: int, rows: int, cols: int, device) -> torch.Tensor:
+    """fp8 code buffer [groups, rows, ld] with ld = cols rounded up to 16, returned as the [groups, rows, cols] view."""
+    ld = (cols + 15) // 16 * 16
+    return torch.zeros((groups, rows, ld), dtype=torch.uint8, device=device)[:, :, :cols]
+
+
+def grouped_mm(x8, w8, offsets, sx, sw, y=None, fmt_x=FP8_E4M3, fmt_w=FP8_E4M3, w_major=FP8_K_MAJOR) -> torch.Tensor:
+    """y[r] = x8[r] w8[e]^T / (sx sw[e]) for the rows offsets[e] <= r < offsets[e + 1] (bf16; the other rows of y are
+    left as they were, or not initialized).  x8 [rows, k] and w8 [groups, n, k] (w_major FP8_MN_MAJOR: [groups, k, n])
+    are fp8 codes, sx one scale, sw one or one per group."""
+    groups = offsets.numel() - 1
+    dev = x8.device
+    (rows, k), ldw = x8.shape, _expert_matrix(w8, groups, "w8")
+    n, kw = (w8.shape[1], w8.shape[2]) if w_major == FP8_K_MAJOR else (w8.shape[2], w8.shape[1])
+    if kw != k or x8.dtype not in _FP8_CODES or w8.dtype not in _FP8_CODES:
+        raise ValueError(f"fp8 codes of one contraction length: got {x8.dtype} {tuple(x8.shape)}, "
+                         f"{w8.dtype} {tuple(w8.shape)}")
+    if sx.numel() != 1:
+        raise ValueError("sx: one scale")
+    g = _groups(offsets, w8.shape[1] * ldw, 0, _scale_step(sw, groups, "sw"))
+    with _on_device(dev, w8, offsets, sx, sw, y):
+        y = _out(y, (rows, n), torch.bfloat16, dev, "y")
+        a = MmArgs(rows, n, k, x8.data_ptr(), fmt_x, FP8_K_MAJOR, _ld(x8), w8.data_ptr(), fmt_w, w_major, ldw,
+                   sx.data_ptr(), sw.data_ptr(), None, 0, None, y.data_ptr(), _ld(y), 0, None, 0)
+        _check(_lib.fp8_mm_grouped(a, FP8_RAGGED_M, g, _stream(dev)), "fp8_mm_grouped")
+    return y
+
+
+def grouped_linear_forward(x, w, offsets, ring_x: ScaleRing | None, ring_w: ScaleRing | None, fmt_x=FP8_E4M3,
+                           fmt_w=FP8_E4M3, x_scale_in=None, w_scale_in=None, hist_len=16, y=None, x8=None,
+                           w8=None) -> ForwardResult:
+    """y = x w[e]^T for the rows of each group e, through fp8_linear_grouped_forward: the linear_forward of a mixture
+    of experts.  x [rows, K] sorted by expert, w [groups, N, K]; either may be bf16/fp16/fp32 or fp8 codes with its
+    *_scale_in (w's: one scale, or one per group).  w8 is [groups, N, K]."""
+    groups = offsets.numel() - 1
+    dev = x.device
+    M, K = x.shape
+    ldw = _expert_matrix(w, groups, "w")
+    N = w.shape[1]
+    if w.shape[2] != K:
+        raise ValueError(f"x and w of one contraction length: {tuple(x.shape)}, {tuple(w.shape)}")
+    xq, wq = x.dtype in _FP8_CODES, w.dtype in _FP8_CODES
+    step = _scale_step(w_scale_in, groups, "w_scale_in") if wq and w_scale_in is not None else 0
+    g = _groups(offsets, 0, 0, step)
+    with _on_device(dev, w, offsets, x_scale_in, w_scale_in, x8, w8, y):
+        y = _out(y, (M, N), torch.bfloat16, dev, "y")
+        if x8 is None:
+            x8 = x.view(torch.uint8) if xq else fp8_alloc(M, K, dev)
+        if w8 is None:
+            w8 = w.view(torch.uint8) if wq else fp8_alloc_experts(groups, N, K, dev)
+        if tuple(x8.shape) != (M, K) or tuple(w8.shape) != (groups, N, K):
+            raise ValueError("x8 [rows, K] and w8 [groups, N, K]")
+        sw_n = groups if step else 1
+        sc = torch.empty(3 + sw_n, dtype=torch.float32, device=dev)
+        sx, amax_x, amax_w, sw = sc[0:1], sc[1:2], sc[2:3], sc[3:]
+        H = ring_x.H if ring_x is not None else (ring_w.H if ring_w is not None else hist_len)
+        args = LinearFwdArgs(
+            M, N, K,
+            _ptr(x), _dtype_code(x, fmt_x), _ld(x), _ptr(x_scale_in),
+            _ptr(w), _dtype_code(w, fmt_w), ldw, _ptr(w_scale_in),
+            None, 0, None,
+            fmt_x, fmt_w, H,
+            _ptr(ring_x.buf) if ring_x is not None else None, _ptr(ring_w.buf) if ring_w is not None else None,
+            _ptr(x8), _ld(x8), _ptr(w8), _expert_matrix(w8, groups, "w8"),
+            _ptr(sx), _ptr(sw), _ptr(amax_x), _ptr(amax_w),
+            _ptr(y), _ld(y))
+        _check(_lib.fp8_linear_grouped_forward(args, g, _stream(dev)), "fp8_linear_grouped_forward")
+    return ForwardResult(y, x8, w8, sx, sw, amax_x, amax_w)
+
+
+def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | None, fmt_g=FP8_E5M2, fmt_x=FP8_E4M3,
+                            fmt_w=FP8_E4M3, need_dx=True, need_dw=True, g_scale_in=None, dx=None, dw=None,
+                            g8=None) -> BackwardResult:
+    """dx [rows, K] and dw [groups, N, K] through fp8_linear_grouped_backward, reusing the forward's x8, w8 and scale
+    snapshots.  Rows of dx outside every group are left as they were (or not initialized)."""
+    groups = offsets.numel() - 1
+    dev = g.device
+    M, N = g.shape
+    x8, w8 = fwd.x8, fwd.w8
+    K = x8.shape[1]
+    ldw = _expert_matrix(w8, groups, "w8")
+    if x8.shape[0] != M or tuple(w8.shape) != (groups, N, K):
+        raise ValueError(f"g {tuple(g.shape)}, x8 {tuple(x8.shape)} and w8 {tuple(w8.shape)} do not fit")
+    gr = _groups(offsets, 0, 0, _scale_step(fwd.sw, groups, "sw"))
+    gq = g.dtype in _FP8_CODES
+    with _on_device(dev, x8, w8, offsets, fwd.sx, fwd.sw, g_scale_in, dx, dw, g8):
+        if g8 is None:
+            g8 = g.view(torch.uint8) if gq else fp8_alloc(M, N, dev)
+        if tuple(g8.shape) != (M, N):
+            raise ValueError("g8 [rows, N]")
+        dx = _out(dx, (M, K), torch.bfloat16, dev, "dx") if need_dx else None
+        dw = _out(dw, (groups, N, K), torch.bfloat16, dev, "dw") if need_dw else None
+        sc = torch.empty(2, dtype=torch.float32, device=dev)
+        args = LinearBwdArgs(
+            M, N, K,
+            _ptr(g), _dtype_code(g, fmt_g), _ld(g), _ptr(g_scale_in),
+            fmt_g, ring_g.H if ring_g is not None else 16, _ptr(ring_g.buf) if ring_g is not None else None,
+            _ptr(g8), _ld(g8), _ptr(sc[0:1]), _ptr(sc[1:2]),
+            _ptr(x8), _ld(x8), _ptr(fwd.sx), fmt_x,
+            _ptr(w8), ldw, _ptr(fwd.sw), fmt_w,
+            int(need_dx), int(need_dw), 0,
+            _ptr(dx), _ld(dx) if need_dx else 0,
+            _ptr(dw), _expert_matrix(dw, groups, "dw") if need_dw else 0,
+            None, None, 0)
+        _check(_lib.fp8_linear_grouped_backward(args, gr, _stream(dev)), "fp8_linear_grouped_backward")
+    return BackwardResult(dx, dw, None, g8, sc[0:1], sc[1:2])
+
+
+def int8_alloc(rows: int, cols: int, device) -> torch.Tensor:
+    """int8 code buffer [rows, ld] with ld = cols rounded up to 16, returned as the [rows, cols] view."""
+    return fp8_alloc(rows, cols, device).view(torch.int8)
+
+
+def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """Rows of x to int8 by their own largest magnitude; returns (codes [rows, cols], scale [rows] fp32).  A weight
+    [N, K] quantized so has one scale per output channel."""
+    dev = x.device
+    rows, cols = x.shape
+    with _on_device(dev, out, scale):
+        out = int8_alloc(rows, cols, dev) if out is None else _out(out, (rows, cols), torch.int8, dev, "out")
+        scale = _out(scale, (rows,), torch.float32, dev, "scale")
+        if not scale.is_contiguous():
+            raise ValueError("scale: contiguous")
+        fp8_quantize_int8(x, out, scale)
+    return out, scale
+
+
+@dataclass
+class Int8Result:
+    y: torch.Tensor
+    x8: torch.Tensor
+    sx: torch.Tensor
+
+
+def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) -> Int8Result:
+    """y = x w^T + bias in 8-bit integers through fp8_linear_int8_forward: x [rows, K] (bf16/fp16/fp32) is quantized
+    row by row, w8 [N, K] int8 and sw [N] come from quantize_int8.  y has x's type unless out_dtype (or y) says
+    otherwise."""
+    dev = x.device
+    (M, K), N = x.shape, w8.shape[0]
+    if w8.dim() != 2 or w8.shape[1] != K or w8.dtype != torch.int8:
+        raise ValueError(f"w8: int8 [N, {K}], got {w8.dtype} {tuple(w8.shape)}")
+    if sw.dtype != torch.float32 or sw.numel() != N or not sw.is_contiguous():
+        raise ValueError(f"sw: {N} contiguous fp32 scales")
+    if bias is not None and (bias.numel() != N or not bias.is_contiguous()):
+        raise ValueError(f"bias: {N} contiguous values")
+    with _on_device(dev, w8, sw, bias, y, x8, sx):
+        y = _out(y, (M, N), out_dtype or (y.dtype if y is not None else x.dtype), dev, "y")
+        if x8 is None:
+            x8 = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :K]
+        sx = _out(sx, (M,), torch.float32, dev, "sx")
+        if tuple(x8.shape) != (M, K) or x8.dtype != torch.int8 or not sx.is_contiguous():
+            raise ValueError("x8 int8 [rows, K], sx contiguous")
+        args = LinearInt8Args(M, N, K, x.data_ptr(), _dtype_code(x), _ld(x), w8.data_ptr(), _ld(w8), sw.data_ptr(),
+                              _ptr(bias), _dtype_code(bias) if bias is not None else 0,
+                              x8.data_ptr(), _ld(x8), sx.data_ptr(), y.data_ptr(), _dtype_code(y), _ld(y))
+        _check(_lib.fp8_linear_int8_forward(args, _stream(dev)), "fp8_linear_int8_forward")
+    return Int8Result(y, x8, sx)

@@ -713,6 +713,243 @@ int validate_quantize(const void* in, int in_dtype, int64_t rows, int64_t cols, 
   return check_fp8_matrix(out, ld_out, rows, cols);
 }
 
+// ---------------------------------------------------------------- grouped and int8 products
+
+// Column tile of a product whose tokens lie on the MMA's N side: `rows` tokens
+// in `groups` groups, tiles_lane 128-row weight tiles.  The smallest tile that
+// holds one and a half times the average group (a larger group takes several
+// tiles, a smaller one a narrower MMA), halved down to 32 while the launch
+// still fits one wave: more CTAs each stream fewer tokens.
+int pick_col_tile(int64_t rows, int64_t groups, int64_t tiles_lane, int sms) {
+  const int64_t live = std::max<int64_t>(1, std::min(groups, rows));
+  const int64_t want = groups == 1 ? rows : (3 * rows / live + 1) / 2;
+  int t = 16;
+  while (t < 256 && t < want) t *= 2;
+  auto tiles = [&](int64_t c) { return ((rows + live - 1) / live + c - 1) / c * live * tiles_lane; };
+  while (t > 32 && tiles(t / 2) <= sms) t /= 2;
+  return t;
+}
+
+struct GroupedCall {
+  int64_t groups = 1;
+  const void* offsets = nullptr;
+  int off64 = 0;
+  int64_t rows = 0;                 // extent of the ragged axis
+  int64_t nlane = 0, ncol = 0, k = 0;
+  const void* lane_op = nullptr; int64_t ld_lane = 0, stride_lane = 0; int lane_mn = 0;
+  const void* col_op = nullptr; int64_t ld_col = 0;
+  int fmt_lane = 0, fmt_col = 0;
+  bool int8 = false, ragged_k = false;
+  const float* scale_a = nullptr; const float* scale_b = nullptr; int scale_b_step = 0;
+  const void* bias = nullptr; int bias_dtype = 0;
+  void* d = nullptr; int d_dtype = FP8_DT_BF16; int64_t ldd = 0, stride_d = 0;
+};
+
+// An upper bound on a launch's tiles: every group may waste one partial tile.
+int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile) {
+  const int64_t tl = (c.nlane + 127) / 128;
+  if (c.ragged_k) return tl * ((c.ncol + col_tile - 1) / col_tile) * c.groups;
+  return tl * (c.rows / col_tile + std::min(c.groups, c.rows));
+}
+
+// One launch of a validated call with at least one group and lane.
+int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = nullptr,
+                const RingFinalize* fin = nullptr, int nfin = 0, const float* sw_src = nullptr,
+                float* sw_dst = nullptr, int sw_n = 0) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const int sms = num_sms(dev);
+  if (sms <= 0 || dev >= 64) return cuda_fail(cudaGetLastError());
+  const int64_t tl = (c.nlane + 127) / 128;
+  int tile;
+  if (c.ragged_k) tile = tl * ((c.ncol + 255) / 256) * c.groups >= sms ? 256 : 128;
+  else tile = pick_col_tile(c.rows, c.groups, tl, sms);
+  GroupedParams p;
+  std::memset(&p, 0, sizeof(p));
+  CUtensorMap maps[3];
+  std::memset(maps, 0, sizeof(maps));
+  int s;
+  if (c.ragged_k) {
+    // both operands MN-major over the ragged rows: (128 elements, 128 rows) boxes
+    if (c.rows > 0) {
+      if ((s = make_fp8_map(&maps[0], c.lane_op, c.nlane, c.rows, c.ld_lane, 128))) return s;
+      if ((s = make_fp8_map(&maps[1], c.col_op, c.ncol, c.rows, c.ld_col, 128))) return s;
+    }
+  } else if (c.k > 0) {
+    const uint64_t batch = c.stride_lane ? static_cast<uint64_t>(c.groups) : 1;
+    s = c.lane_mn ? make_fp8_map(&maps[0], c.lane_op, c.nlane, c.k, c.ld_lane, 128, batch, c.stride_lane)
+                  : make_fp8_map(&maps[0], c.lane_op, c.k, c.nlane, c.ld_lane, 128, batch, c.stride_lane);
+    if (s) return s;
+    if ((s = make_fp8_map(&maps[1], c.col_op, c.k, c.rows, c.ld_col, static_cast<uint32_t>(tile)))) return s;
+    if ((s = make_fp8_map(&maps[2], c.col_op, c.k, c.rows, c.ld_col, 32))) return s;
+  }
+  p.groups = static_cast<int>(c.groups);
+  p.rows = static_cast<int>(c.rows);
+  p.offsets = c.offsets;
+  p.off64 = c.off64;
+  p.nlane = static_cast<int>(c.nlane);
+  p.ncol = static_cast<int>(c.ncol);
+  p.tiles_lane = static_cast<int>(tl);
+  p.tiles_col = c.ragged_k ? static_cast<int>((c.ncol + tile - 1) / tile) : 0;
+  p.k_blocks = static_cast<int>(((c.ragged_k ? c.rows : c.k) + 127) / 128);
+  p.lane_shared = c.stride_lane == 0 ? 1 : 0;
+  p.col_tile = tile;
+  p.stages = grouped_stages(tile);
+  p.lane_mn = c.lane_mn;
+  p.idesc = c.int8 ? idesc_i8(128, 0) : idesc_f8(c.fmt_lane, c.fmt_col, c.lane_mn, c.ragged_k ? 1 : 0, 128, 0);
+  p.scale_a = c.scale_a;
+  p.scale_b = c.scale_b;
+  p.scale_b_step = c.scale_b_step;
+  p.bias = c.bias;
+  p.bias_dtype = c.bias_dtype;
+  p.d = c.d;
+  p.ldd = c.ldd;
+  p.stride_d = c.ragged_k ? c.stride_d : 0;
+  p.vec_ok = aligned(c.d, 16) && (c.ldd * 2) % 16 == 0 && (p.stride_d * 2) % 16 == 0;
+  p.status = status_ptr(dev);
+  if (side) p.side = *side;
+  for (int i = 0; i < nfin; ++i) p.fin[i] = fin[i];
+  p.nfin = nfin;
+  p.sw_src = sw_src;
+  p.sw_dst = sw_dst;
+  p.sw_n = sw_n;
+  e = launch_grouped(maps, p, c.int8, c.ragged_k, c.d_dtype, grouped_max_tiles(c, tile), st);
+  return e == cudaSuccess ? FP8_OK : cuda_fail(e);
+}
+
+int validate_groups(const fp8_groups* g) {
+  if (!g || g->groups < 0) return FP8_ERR_INVALID_ARG;
+  if (g->groups > FP8_MAX_GROUPS) return FP8_ERR_TOO_LARGE;
+  if (g->offsets_64 != 0 && g->offsets_64 != 1) return FP8_ERR_INVALID_ARG;
+  if (g->scale_b_step != 0 && g->scale_b_step != 1) return FP8_ERR_INVALID_ARG;
+  if (g->stride_b < 0 || g->stride_d < 0) return FP8_ERR_INVALID_ARG;
+  if (g->groups > 0 && (!g->offsets || !aligned(g->offsets, g->offsets_64 ? 8 : 4))) return FP8_ERR_INVALID_ARG;
+  return FP8_OK;
+}
+
+constexpr int64_t kMaxTiles = int64_t(1) << 30;
+
+// Checks a grouped product and turns it into a kernel call.  The weight (or,
+// for a ragged contraction, X: the operand along D's contiguous axis) is the
+// lane operand, which is fp8_mm's B in both forms.
+int grouped_call(const fp8_mm_args& a, int ragged, const fp8_groups& g, GroupedCall* out) {
+  if (ragged != FP8_RAGGED_M && ragged != FP8_RAGGED_K) return FP8_ERR_INVALID_ARG;
+  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > kMaxDim || a.n > kMaxDim || a.k > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (!is_fmt(a.fmt_a) || !is_fmt(a.fmt_b) || !a.scale_a || !a.scale_b) return FP8_ERR_INVALID_ARG;
+  if ((a.a_major != FP8_K_MAJOR && a.a_major != FP8_MN_MAJOR) || (a.b_major != FP8_K_MAJOR && a.b_major != FP8_MN_MAJOR))
+    return FP8_ERR_INVALID_ARG;
+  const bool rk = ragged == FP8_RAGGED_K;
+  if (a.a_major != (rk ? FP8_MN_MAJOR : FP8_K_MAJOR) || (rk && a.b_major != FP8_MN_MAJOR)) return FP8_ERR_UNSUPPORTED;
+  if (a.bias || a.tile_cfg != FP8_TILE_AUTO) return FP8_ERR_UNSUPPORTED;
+  int s = rk ? check_fp8_matrix(a.a, a.lda, a.k, a.m) : check_fp8_matrix(a.a, a.lda, a.m, a.k);
+  if (s) return s;
+  if (g.groups > 0) {
+    s = a.b_major == FP8_K_MAJOR ? check_fp8_matrix(a.b, a.ldb, a.n, a.k) : check_fp8_matrix(a.b, a.ldb, a.k, a.n);
+    if (s) return s;
+  }
+  if (g.groups > 0 && a.m > 0 && a.n > 0 && (!a.d || a.ldd < a.n || !aligned(a.d, 2))) return FP8_ERR_INVALID_ARG;
+  if (!rk && g.groups > 1) {
+    if (g.stride_b % 16) return FP8_ERR_MISALIGNED;
+    const int64_t outer = a.b_major == FP8_K_MAJOR ? a.n : a.k;
+    // stride 0 shares one B; other strides keep the groups' matrices apart
+    if (g.stride_b != 0 && outer > 0 && g.stride_b < outer * a.ldb - a.ldb + (a.b_major == FP8_K_MAJOR ? a.k : a.n))
+      return FP8_ERR_INVALID_ARG;
+  }
+  if (rk && g.groups > 1 && a.m > 0 && g.stride_d < (a.m - 1) * a.ldd + a.n) return FP8_ERR_INVALID_ARG;
+  GroupedCall c;
+  c.groups = g.groups;
+  c.offsets = g.offsets;
+  c.off64 = g.offsets_64;
+  c.rows = rk ? a.k : a.m;
+  c.nlane = a.n;
+  c.ncol = rk ? a.m : 0;
+  c.k = rk ? 0 : a.k;
+  c.lane_op = a.b;
+  c.ld_lane = a.ldb;
+  c.stride_lane = g.stride_b;
+  c.lane_mn = a.b_major == FP8_MN_MAJOR ? 1 : 0;
+  c.col_op = a.a;
+  c.ld_col = a.lda;
+  c.fmt_lane = a.fmt_b;
+  c.fmt_col = a.fmt_a;
+  c.ragged_k = rk;
+  c.scale_a = a.scale_a;
+  c.scale_b = a.scale_b;
+  c.scale_b_step = g.scale_b_step;
+  c.d = a.d;
+  c.ldd = a.ldd;
+  c.stride_d = g.stride_d;
+  // 32-bit tile indexes, at the smallest column tile either form may take
+  if (a.n > 0 && g.groups > 0 && grouped_max_tiles(c, rk ? 128 : 16) > kMaxTiles) return FP8_ERR_INVALID_ARG;
+  *out = c;
+  return FP8_OK;
+}
+
+bool grouped_live(const GroupedCall& c) {
+  return c.groups > 0 && c.nlane > 0 && (c.ragged_k ? c.ncol > 0 : c.rows > 0);
+}
+
+int validate_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, int64_t ld_in, const int8_t* out,
+                           int64_t ld_out, const float* scale) {
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (!is_wide(in_dtype)) return FP8_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  if (!in || !scale || !aligned(in, esize(in_dtype)) || !aligned(scale, 4) || ld_in < cols) return FP8_ERR_INVALID_ARG;
+  return check_fp8_matrix(out, ld_out, rows, cols);
+}
+
+int run_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, int64_t ld_in, int8_t* out,
+                      int64_t ld_out, float* scale, cudaStream_t st) {
+  Int8QuantizeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.in = in;
+  p.rows = rows;
+  p.cols = cols;
+  p.ld_in = ld_in;
+  p.out = out;
+  p.ld_out = ld_out;
+  p.scale = scale;
+  p.vec_ok = aligned(in, 16) && (ld_in * esize(in_dtype)) % 16 == 0;
+  cudaError_t e = launch_quantize_int8(in_dtype, p, st);
+  return e == cudaSuccess ? FP8_OK : cuda_fail(e);
+}
+
+int int8_call(const fp8_mm_int8_args& a, GroupedCall* out) {
+  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > kMaxDim || a.n > kMaxDim || a.k > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (a.k > FP8_MAX_INT8_K) return FP8_ERR_TOO_LARGE;
+  if (!is_wide(a.d_dtype)) return FP8_ERR_INVALID_ARG;
+  if (a.bias && (!is_wide(a.bias_dtype) || !aligned(a.bias, esize(a.bias_dtype)))) return FP8_ERR_INVALID_ARG;
+  int s = check_fp8_matrix(a.a, a.lda, a.m, a.k);
+  if (s) return s;
+  if ((s = check_fp8_matrix(a.b, a.ldb, a.n, a.k))) return s;
+  if (a.m > 0 && a.n > 0) {
+    // an empty contraction reads no scales
+    if (a.k > 0 && (!a.scale_a || !a.scale_b || !aligned(a.scale_a, 4) || !aligned(a.scale_b, 4)))
+      return FP8_ERR_INVALID_ARG;
+    if (!a.d || a.ldd < a.n || !aligned(a.d, esize(a.d_dtype))) return FP8_ERR_INVALID_ARG;
+  }
+  GroupedCall c;
+  c.rows = a.m;
+  c.nlane = a.n;
+  c.k = a.k;
+  c.lane_op = a.b;
+  c.ld_lane = a.ldb;
+  c.col_op = a.a;
+  c.ld_col = a.lda;
+  c.int8 = true;
+  c.scale_a = a.scale_a;
+  c.scale_b = a.scale_b;
+  c.bias = a.bias;
+  c.bias_dtype = a.bias_dtype;
+  c.d = a.d;
+  c.d_dtype = a.d_dtype;
+  c.ldd = a.ldd;
+  if (a.m > 0 && a.n > 0 && grouped_max_tiles(c, 16) > kMaxTiles) return FP8_ERR_INVALID_ARG;
+  *out = c;
+  return FP8_OK;
+}
+
 }  // namespace
 
 int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
@@ -1131,6 +1368,216 @@ int fp8_linear_backward(const fp8_linear_bwd_args* a, fp8_stream_t stream) {
   return FP8_OK;
 }
 
+int fp8_mm_grouped(const fp8_mm_args* a, int ragged, const fp8_groups* g, fp8_stream_t stream) {
+  if (!a) return FP8_ERR_INVALID_ARG;
+  int s = validate_groups(g);
+  if (s) return s;
+  GroupedCall c;
+  if ((s = grouped_call(*a, ragged, *g, &c))) return s;
+  if (!grouped_live(c)) return FP8_OK;
+  return run_grouped(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fp8_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, int64_t ld_in, int8_t* out,
+                      int64_t ld_out, float* scale, fp8_stream_t stream) {
+  int s = validate_quantize_int8(in, in_dtype, rows, cols, ld_in, out, ld_out, scale);
+  if (s) return s;
+  if (rows == 0 || cols == 0) return FP8_OK;
+  return run_quantize_int8(in, in_dtype, rows, cols, ld_in, out, ld_out, scale, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fp8_mm_int8(const fp8_mm_int8_args* a, fp8_stream_t stream) {
+  if (!a) return FP8_ERR_INVALID_ARG;
+  GroupedCall c;
+  int s = int8_call(*a, &c);
+  if (s) return s;
+  if (!grouped_live(c)) return FP8_OK;
+  return run_grouped(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fp8_linear_int8_forward(const fp8_linear_int8_args* a, fp8_stream_t stream) {
+  if (!a) return FP8_ERR_INVALID_ARG;
+  int s = validate_quantize_int8(a->x, a->x_dtype, a->M, a->K, a->ldx, a->x8, a->ldx8, a->sx_out);
+  if (s) return s;
+  const fp8_mm_int8_args mm = {a->M, a->N, a->K, a->x8, a->ldx8, a->w8, a->ldw8, a->sx_out, a->sw,
+                               a->bias, a->bias_dtype, a->y, a->y_dtype, a->ldy};
+  GroupedCall c;
+  if ((s = int8_call(mm, &c))) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (a->M > 0 && a->K > 0 &&
+      (s = run_quantize_int8(a->x, a->x_dtype, a->M, a->K, a->ldx, a->x8, a->ldx8, a->sx_out, st)))
+    return s;
+  if (!grouped_live(c)) return FP8_OK;
+  return run_grouped(c, st);
+}
+
+int fp8_linear_grouped_forward(const fp8_linear_fwd_args* a, const fp8_groups* g, fp8_stream_t stream) {
+  if (!a) return FP8_ERR_INVALID_ARG;
+  int s = validate_groups(g);
+  if (s) return s;
+  const int64_t M = a->M, N = a->N, K = a->K, E = g->groups;
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (g->stride_b != 0 || g->stride_d != 0) return FP8_ERR_INVALID_ARG;
+  if (!is_fmt(a->fmt_x) || !is_fmt(a->fmt_w)) return FP8_ERR_INVALID_ARG;
+  if (!a->sx_out || !a->sw_out) return FP8_ERR_INVALID_ARG;
+  if (a->bias) return FP8_ERR_UNSUPPORTED;
+  const bool xq = is_fp8(a->x_dtype), wq = is_fp8(a->w_dtype);
+  if ((!xq && !is_wide(a->x_dtype)) || (!wq && !is_wide(a->w_dtype))) return FP8_ERR_INVALID_ARG;
+  if (!wq && g->scale_b_step) return FP8_ERR_INVALID_ARG;
+  const int64_t wrows = N * E;
+  if (xq) {
+    if (a->x_dtype - FP8_DT_E4M3 != a->fmt_x || !a->x_scale_in) return FP8_ERR_INVALID_ARG;
+    if ((s = check_fp8_matrix(a->x, a->ldx, M, K))) return s;
+  } else if ((s = validate_quantize(a->x, a->x_dtype, M, K, a->ldx, a->fmt_x, a->ring_x, a->hist_len, a->x8,
+                                    a->ldx8, a->amax_x_out))) {
+    return s;
+  }
+  if (wq) {
+    if (a->w_dtype - FP8_DT_E4M3 != a->fmt_w || !a->w_scale_in) return FP8_ERR_INVALID_ARG;
+    if ((s = check_fp8_matrix(a->w, a->ldw, wrows, K))) return s;
+  } else if ((s = validate_quantize(a->w, a->w_dtype, wrows, K, a->ldw, a->fmt_w, a->ring_w, a->hist_len, a->w8,
+                                    a->ldw8, a->amax_w_out))) {
+    return s;
+  }
+  if (!xq && !wq && a->ring_x && a->ring_x == a->ring_w) return FP8_ERR_INVALID_ARG;
+  if (!xq && !wq && !a->ring_x && !a->ring_w && a->amax_x_out == a->amax_w_out) return FP8_ERR_INVALID_ARG;
+  fp8_mm_args mm;
+  std::memset(&mm, 0, sizeof(mm));
+  mm.m = M; mm.n = N; mm.k = K;
+  mm.a = xq ? static_cast<const uint8_t*>(a->x) : a->x8; mm.fmt_a = a->fmt_x; mm.lda = xq ? a->ldx : a->ldx8;
+  mm.b = wq ? static_cast<const uint8_t*>(a->w) : a->w8; mm.fmt_b = a->fmt_w; mm.ldb = wq ? a->ldw : a->ldw8;
+  mm.scale_a = xq ? a->x_scale_in : a->sx_out;
+  mm.scale_b = wq ? a->w_scale_in : a->sw_out;
+  mm.d = a->y; mm.ldd = a->ldy;
+  fp8_groups gm = *g;
+  gm.stride_b = N * mm.ldb;
+  GroupedCall c;
+  if ((s = grouped_call(mm, FP8_RAGGED_M, gm, &c))) return s;
+
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // An empty operand is neither quantized nor side-written, as in
+  // fp8_linear_forward; its ring does not step.
+  const bool x_live = M > 0 && K > 0, w_live = wrows > 0 && K > 0;
+  const bool gemm = grouped_live(c);
+  SideWrites side;
+  std::memset(&side, 0, sizeof(side));
+  if (xq && x_live) { side.copy_src[0] = a->x_scale_in; side.copy_dst[0] = a->sx_out; side.zero_dst[0] = a->amax_x_out; }
+  if (wq && w_live) side.zero_dst[1] = a->amax_w_out;
+  const int sw_n = wq && w_live ? (g->scale_b_step ? static_cast<int>(E) : 1) : 0;
+  RingFinalize fin[2];
+  int nfin = 0;
+  const bool quant_x = !xq && x_live, quant_w = !wq && w_live;
+  if (gemm && quant_x && a->ring_x) fin[nfin++] = ring_fin(a->ring_x, a->hist_len, a->fmt_x, a->amax_x_out);
+  if (gemm && quant_w && a->ring_w) fin[nfin++] = ring_fin(a->ring_w, a->hist_len, a->fmt_w, a->amax_w_out);
+  if (quant_x && quant_w && a->x_dtype == a->w_dtype && a->fmt_x == a->fmt_w) {
+    QuantizeParams qx = make_qparams(a->x, a->x_dtype, M, K, a->ldx, a->fmt_x, a->ring_x, a->hist_len, a->x8,
+                                     a->ldx8, a->amax_x_out, a->sx_out, true);
+    QuantizeParams qw = make_qparams(a->w, a->w_dtype, wrows, K, a->ldw, a->fmt_w, a->ring_w, a->hist_len, a->w8,
+                                     a->ldw8, a->amax_w_out, a->sw_out, true);
+    qx.defer_finalize = gemm && a->ring_x ? 1 : 0;
+    qw.defer_finalize = gemm && a->ring_w ? 1 : 0;
+    if ((s = amax_pass(a->x_dtype, &qx, &qw, st))) return s;
+    cudaError_t e = launch_quantize(a->x_dtype, a->fmt_x, &qx, &qw, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+  } else {
+    if (quant_x && (s = run_quantize(a->x, a->x_dtype, M, K, a->ldx, a->fmt_x, a->ring_x, a->hist_len, a->x8,
+                                     a->ldx8, a->amax_x_out, a->sx_out, st, gemm)))
+      return s;
+    if (quant_w && (s = run_quantize(a->w, a->w_dtype, wrows, K, a->ldw, a->fmt_w, a->ring_w, a->hist_len, a->w8,
+                                     a->ldw8, a->amax_w_out, a->sw_out, st, gemm)))
+      return s;
+  }
+  if (gemm) return run_grouped(c, st, &side, fin, nfin, a->w_scale_in, a->sw_out, sw_n);
+  if (sw_n) {  // no product follows (M = 0): the snapshot of w's scales alone
+    cudaError_t e = cudaMemcpyAsync(a->sw_out, a->w_scale_in, static_cast<size_t>(sw_n) * 4, cudaMemcpyDeviceToDevice, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  if (side.copy_dst[0] || side.zero_dst[1]) {
+    cudaError_t e = launch_side_writes(side, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return FP8_OK;
+}
+
+int fp8_linear_grouped_backward(const fp8_linear_bwd_args* a, const fp8_groups* g, fp8_stream_t stream) {
+  if (!a) return FP8_ERR_INVALID_ARG;
+  int s = validate_groups(g);
+  if (s) return s;
+  const int64_t M = a->M, N = a->N, K = a->K;
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (g->stride_b != 0 || g->stride_d != 0) return FP8_ERR_INVALID_ARG;
+  if (!is_fmt(a->fmt_g) || !is_fmt(a->fmt_x) || !is_fmt(a->fmt_w)) return FP8_ERR_INVALID_ARG;
+  if (!a->sg_out || (M > 0 && N > 0 && !a->g)) return FP8_ERR_INVALID_ARG;
+  if (a->need_dbias) return FP8_ERR_UNSUPPORTED;
+  const bool gq = is_fp8(a->g_dtype);
+  if (!gq && !is_wide(a->g_dtype)) return FP8_ERR_INVALID_ARG;
+  if (gq) {
+    if (a->g_dtype - FP8_DT_E4M3 != a->fmt_g || !a->g_scale_in) return FP8_ERR_INVALID_ARG;
+    if ((s = check_fp8_matrix(a->g, a->ldg, M, N))) return s;
+  } else if ((s = validate_quantize(a->g, a->g_dtype, M, N, a->ldg, a->fmt_g, a->ring_g, a->hist_len, a->g8,
+                                    a->ldg8, a->amax_g_out))) {
+    return s;
+  }
+  fp8_mm_args mx, mw;
+  std::memset(&mx, 0, sizeof(mx));
+  mx.a = gq ? static_cast<const uint8_t*>(a->g) : a->g8;
+  mx.fmt_a = a->fmt_g;
+  mx.lda = gq ? a->ldg : a->ldg8;
+  mx.scale_a = gq ? a->g_scale_in : a->sg_out;
+  mw = mx;
+  // dX[r, k] = sum_n G8[r, n] W8_e[n, k]: W8_e is MN-major (k contiguous)
+  mx.m = M; mx.n = K; mx.k = N;
+  mx.b = a->w8; mx.fmt_b = a->fmt_w; mx.b_major = FP8_MN_MAJOR; mx.ldb = a->ldw8;
+  mx.scale_b = a->sw;
+  mx.d = a->dx; mx.ldd = a->lddx;
+  // dW_e[n, k] = sum_{r in e} G8[r, n] X8[r, k]
+  mw.m = N; mw.n = K; mw.k = M;
+  mw.a_major = FP8_MN_MAJOR;
+  mw.b = a->x8; mw.fmt_b = a->fmt_x; mw.b_major = FP8_MN_MAJOR; mw.ldb = a->ldx8;
+  mw.scale_b = a->sx;
+  mw.d = a->dw; mw.ldd = a->lddw;
+  fp8_groups gx = *g, gw = *g;
+  gx.stride_b = N * a->ldw8;
+  gw.stride_d = N * a->lddw;
+  gw.scale_b_step = 0;
+  GroupedCall cx, cw;
+  if (a->need_dx && (s = grouped_call(mx, FP8_RAGGED_M, gx, &cx))) return s;
+  if (a->need_dw && (s = grouped_call(mw, FP8_RAGGED_K, gw, &cw))) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool g_live = M > 0 && N > 0;
+  const bool dx_live = a->need_dx && grouped_live(cx), dw_live = a->need_dw && grouped_live(cw);
+  // The first product of the two finishes g's ring step or writes its snapshot.
+  SideWrites side;
+  std::memset(&side, 0, sizeof(side));
+  RingFinalize fin[1];
+  int nfin = 0;
+  bool side_pending = false;
+  if (g_live && gq) {
+    side.copy_src[0] = a->g_scale_in; side.copy_dst[0] = a->sg_out; side.zero_dst[0] = a->amax_g_out;
+    side_pending = true;
+  } else if (g_live) {
+    const bool follows = dx_live || dw_live;
+    if (follows && a->ring_g) fin[nfin++] = ring_fin(a->ring_g, a->hist_len, a->fmt_g, a->amax_g_out);
+    if ((s = run_quantize(a->g, a->g_dtype, M, N, a->ldg, a->fmt_g, a->ring_g, a->hist_len, a->g8, a->ldg8,
+                          a->amax_g_out, a->sg_out, st, follows)))
+      return s;
+  }
+  if (dx_live) {
+    if ((s = run_grouped(cx, st, side_pending ? &side : nullptr, fin, nfin))) return s;
+    side_pending = false;
+    nfin = 0;
+  }
+  if (dw_live) {
+    if ((s = run_grouped(cw, st, side_pending ? &side : nullptr, fin, nfin))) return s;
+    side_pending = false;
+  }
+  if (side_pending) {
+    cudaError_t e = launch_side_writes(side, st);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return FP8_OK;
+}
+
 int fp8_wait_selftest(const void* flag, uint64_t limit_ns, int* results, fp8_stream_t stream) {
   if (!flag || !results || !aligned(flag, 4) || !aligned(results, 4)) return FP8_ERR_INVALID_ARG;
   if (limit_ns == 0 || limit_ns > 2000000000ull) return FP8_ERR_INVALID_ARG;
@@ -1169,7 +1616,7 @@ const char* fp8_status_string(int status) {
     case FP8_ERR_CUDA: return g_err[0] ? g_err : "CUDA error";
     case FP8_ERR_DEVICE_TIMEOUT: return "a kernel gave up on a bounded wait";
     case FP8_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
-    case FP8_ERR_TOO_LARGE: return "request exceeds the fixed scratch of a no-allocation entry point";
+    case FP8_ERR_TOO_LARGE: return "request beyond a fixed limit (scratch of a no-allocation entry point, groups, int8 k)";
     default: return "unknown status";
   }
 }

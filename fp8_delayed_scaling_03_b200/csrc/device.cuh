@@ -243,6 +243,15 @@ __host__ __device__ constexpr uint32_t idesc_f8(int fmt_a, int fmt_b, int major_
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// Instruction descriptor for kind::i8, dense: signed 8-bit operands, both
+// K-major, int32 accumulator without saturation.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4)                                   // D format: s32
+         | (1u << 7) | (1u << 10)                    // A, B: signed 8-bit
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
 // ---------------------------------------------------------------- CTA pairs
 // A cluster of two CTAs runs one 2-SM MMA tile (tcgen05 cta_group::2).  Every
 // CTA loads only its own operand halves into its own shared memory (no load is

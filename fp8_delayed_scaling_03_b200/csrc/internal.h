@@ -160,6 +160,51 @@ struct FillParams {
   const float* bias_scale;
 };
 
+// A product of tokens with 8-bit weights that carry scales of their own
+// (grouped.cu).  The lane axis is the output's contiguous one, the column
+// axis its rows.
+constexpr int kMaxGroups = 1024;
+struct GroupedParams {
+  int groups;                 // 1 with offsets == nullptr: the rows [0, rows)
+  int rows;                   // extent of the ragged axis in its buffers; offsets are clamped to it
+  const void* offsets;        // device [groups + 1], int32 or (off64) int64
+  int off64;
+  int nlane;                  // lanes: the output's columns
+  int ncol;                   // ragged contraction: output rows of each group
+  int tiles_lane, tiles_col;  // tiles_col: ragged contraction only
+  int k_blocks;               // 128-byte blocks of the contraction (ragged contraction: of all rows)
+  int col_tile;               // columns per tile: 16, 32, 64, 128 or 256
+  int stages;
+  int lane_mn;                // the lane operand is MN-major
+  int lane_shared;            // every group uses the same lane operand: batch coordinate 0
+  uint32_t idesc;             // without N, which follows each tile's columns
+  const float* scale_a;       // fp8: one scale; int8: one per column (token)
+  const float* scale_b;       // fp8: one per group or (step 0) one; int8: one per lane (channel)
+  int scale_b_step;
+  const void* bias;           // int8: per lane, or NULL
+  int bias_dtype;
+  void* d;
+  int64_t ldd, stride_d;      // elements; stride_d between groups (ragged contraction)
+  int vec_ok;                 // 16-byte stores can address D's rows
+  int* status;
+  SideWrites side;
+  RingFinalize fin[2];
+  int nfin;
+  const float* sw_src;        // per-group scale snapshot: sw_dst[i] = sw_src[i], i < sw_n
+  float* sw_dst;
+  int sw_n;
+};
+
+// Quantize of each row to 8-bit integers by its own largest magnitude.
+struct Int8QuantizeParams {
+  const void* in;
+  int64_t rows, cols, ld_in;
+  int8_t* out;
+  int64_t ld_out;
+  float* scale;               // [rows]
+  int vec_ok;                 // 16-byte loads can address the rows
+};
+
 struct DbiasParams {
   const void* g;
   int dtype;
@@ -198,6 +243,14 @@ int gemm_split_factor(int tiles, int k_blocks, int sms, bool forced);
 int gemm_pair_capacity(int device);
 // maps[0..2]: A, B, D of pr[0]; maps[3..5]: those of pr[1] (zeroed if unused).
 cudaError_t launch_gemm(const CUtensorMap* maps, const GemmParams& p, int cfg, cudaStream_t s);
+// Stages of the operand ring for a column tile.
+int grouped_stages(int col_tile);
+// maps: lane operand, column operand (box of col_tile rows), column operand
+// (box of 32 rows; unused by a ragged contraction).  max_tiles: an upper bound
+// on the launch's tiles.  out_dtype: kBF16, or for int8 also kFP16 / kFP32.
+cudaError_t launch_grouped(const CUtensorMap* maps, const GroupedParams& p, bool int8, bool ragged_k, int out_dtype,
+                           int64_t max_tiles, cudaStream_t s);
+cudaError_t launch_quantize_int8(int in_dtype, const Int8QuantizeParams& p, cudaStream_t s);
 cudaError_t launch_dbias(const DbiasParams& p, cudaStream_t s);
 cudaError_t launch_fill(const FillParams& p, cudaStream_t s);
 cudaError_t launch_wait_selftest(const uint32_t* flag, int* status, int* results, uint64_t limit_ns,

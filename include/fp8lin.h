@@ -98,7 +98,7 @@ typedef enum {
   FP8_ERR_CUDA = -4,           /* a CUDA call failed (see fp8_status_string)    */
   FP8_ERR_DEVICE_TIMEOUT = -5, /* a kernel gave up on a bounded wait            */
   FP8_ERR_WORKSPACE = -6,      /* workspace missing or smaller than required    */
-  FP8_ERR_TOO_LARGE = -7       /* beyond the fixed scratch of a no-allocation entry point */
+  FP8_ERR_TOO_LARGE = -7       /* beyond a fixed limit: the scratch of a no-allocation entry point, groups, int8 k */
 } fp8_status;
 
 /* ------------------------------------------------------------------ rings
@@ -257,6 +257,83 @@ FP8LIN_API size_t fp8_mm_workspace_bytes(int64_t m, int64_t n, int64_t k);
 FP8LIN_API int fp8_mm_batched(const fp8_mm_args* args, int64_t batch, int64_t stride_a, int64_t stride_b,
                               int64_t stride_d, fp8_stream_t stream);
 
+/* ---------------------------------------------------------------- grouped mm
+ * FP8 products grouped by expert with ragged sizes: the rows of one matrix are
+ * sorted by group and each group has a weight of its own.  The group bounds
+ * live on the DEVICE, so a router's counts never come back to the host:
+ *   groups    number of groups, 0 .. FP8_MAX_GROUPS (FP8_ERR_TOO_LARGE above)
+ *   offsets   device [groups + 1], non-decreasing: group e is the rows
+ *             offsets[e] <= r < offsets[e + 1].  Empty groups are fine, and so
+ *             are rows before offsets[0] and behind offsets[groups].  Offsets
+ *             are clamped to [0, rows] and a smaller one counts as its
+ *             predecessor, so that no value can lead outside the buffers.
+ *   offsets_64  0: int32 offsets, 1: int64 (aligned to their size)
+ *   stride_b  ELEMENTS between the groups' B matrices (FP8_RAGGED_M), a
+ *             multiple of 16
+ *   stride_d  ELEMENTS between the groups' D matrices (FP8_RAGGED_K), at least
+ *             (m - 1) * ldd + n
+ *   scale_b_step  0: args->scale_b is one scale; 1: one per group
+ * fp8_mm_grouped applies fp8_mm's arithmetic to every group e:
+ *   FP8_RAGGED_M: m is ragged.  D[r, j] = bf16_rne( (sum_k A(r,k) B_e(j,k)) /
+ *     (scale_a * scale_b[e * scale_b_step]) ) for the rows r of e.  args->m is
+ *     the number of rows of the A and D buffers, A is K-major, B_e = b + e *
+ *     stride_b is K-major (the forward, X W_e^T) or MN-major (dX, G W_e).
+ *     Rows of D outside every group are left as they were.
+ *   FP8_RAGGED_K: the contraction is ragged.  D_e[i, j] = bf16_rne( (sum_{r in
+ *     e} A(i,r) B(j,r)) / (scale_a * scale_b[...]) ), the weight gradient
+ *     dW_e = G_e^T X_e.  args->k is the number of rows of the A and B buffers,
+ *     both MN-major; D_e = d + e * stride_d, zero for an empty group.
+ * The other majors, a bias and a forced tile_cfg (FP8_TILE_AUTO only) are
+ * FP8_ERR_UNSUPPORTED.  One launch, no workspace, deterministic: a row's
+ * result does not depend on where its group lies or on the other groups. */
+#define FP8_MAX_GROUPS 1024
+typedef enum { FP8_RAGGED_M = 0, FP8_RAGGED_K = 1 } fp8_ragged;
+typedef struct fp8_groups {
+  int64_t groups;
+  const void* offsets; int offsets_64;
+  int64_t stride_b, stride_d;
+  int scale_b_step;
+} fp8_groups;
+FP8LIN_API int fp8_mm_grouped(const fp8_mm_args* args, int ragged, const fp8_groups* groups, fp8_stream_t stream);
+
+/* ---------------------------------------------------------------- int8
+ * 8-bit integers with a scale for each row: serving a linear in W8A8, tokens
+ * scaled row by row and weights channel by channel. */
+
+/* Each row by its own largest magnitude:
+ *   amax = max_c |in[r, c]|, scale[r] = amax / 127 (fp32),
+ *   out[r, c] = the integer nearest to 127 in[r, c] / amax (ties to even, the
+ *   quotient taken exactly), |out| <= 127.
+ * A row of zeros gets scale 1 and codes 0; a row that holds a NaN or an
+ * infinity gets scale NaN and codes 0, so that every product with it is NaN.
+ *   in     bf16/fp16/fp32 [rows, ld_in]
+ *   out    int8 [rows, ld_out], ld_out % 16 == 0, 16-byte aligned; the bytes
+ *          from cols up to the next multiple of 16 are written 0
+ *   scale  device fp32 [rows], required (cols = 0: left as it was) */
+FP8LIN_API int fp8_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, int64_t ld_in,
+                                 int8_t* out, int64_t ld_out, float* scale, fp8_stream_t stream);
+
+/* D[i, j] = round( ((float)(sum_k A[i,k] B[j,k]) * scale_a[i]) * scale_b[j] + bias[j] )
+ * The sum is exact in int32 (tcgen05, kind::i8); k > FP8_MAX_INT8_K could
+ * overflow it and returns FP8_ERR_TOO_LARGE.  Its conversion and the two
+ * products are each rounded to fp32, then the one rounding to D's type.
+ *   a        int8 [m, lda], b int8 [n, ldb]: both K-major, ld % 16 == 0, base
+ *            16-byte aligned (as the fp8 matrices)
+ *   scale_a  device fp32 [m], scale_b device fp32 [n]
+ *   bias     optional [n], bias_dtype FP8_DT_BF16/FP16/FP32
+ *   d        [m, ldd] of d_dtype FP8_DT_BF16/FP16/FP32, ldd >= n
+ * k = 0: every sum is empty, D = bias (or 0); the scales are not read. */
+#define FP8_MAX_INT8_K 131071
+typedef struct fp8_mm_int8_args {
+  int64_t m, n, k;
+  const int8_t* a; int64_t lda;
+  const int8_t* b; int64_t ldb;
+  const float* scale_a; const float* scale_b;
+  const void* bias; int bias_dtype;
+  void* d; int d_dtype; int64_t ldd;
+} fp8_mm_int8_args;
+FP8LIN_API int fp8_mm_int8(const fp8_mm_int8_args* args, fp8_stream_t stream);
+
 /* Two independent GEMMs (the backward's dX and dW) in ONE launch over one
  * persistent tile schedule.  Same results as two fp8_mm calls; the tile
  * configuration (a->tile_cfg, or chosen for the pair when AUTO) and, for
@@ -384,6 +461,41 @@ typedef struct fp8_linear_bwd_args {
   void* workspace; size_t workspace_bytes;
 } fp8_linear_bwd_args;
 FP8LIN_API int fp8_linear_backward(const fp8_linear_bwd_args* args, fp8_stream_t stream);
+
+/* The linears of a mixture of experts: fp8_linear_forward / _backward with x
+ * and g sorted by expert and one weight per group.  M is the number of rows of
+ * the x, g, y and dx buffers, N and K are one expert's sizes, and the weights
+ * (w, w8) and dw hold the groups one after another: [groups * N, ld], N rows
+ * each.  groups->groups, offsets and offsets_64 as in fp8_mm_grouped; its
+ * strides must be 0 (they follow from N and ld).
+ *   y  = bf16( X8 W8_e^T / (sx sw) )   rows of group e; others left as they were
+ *   dx = bf16( G8 W8_e / (sg sw) )     rows of group e; others left as they were
+ *   dw_e = bf16( G8_e^T X8_e / (sg sx) ), zero for an empty group
+ * x and g are quantized whole with their rings: rows outside every group
+ * enter the amax, so keep them finite (zero).  w is quantized as one tensor
+ * with one ring (scale_b_step 0); a pre-quantized w may come with one scale
+ * per group instead (scale_b_step 1): then w_scale_in, sw_out and the
+ * backward's sw hold `groups` values.  scale_b_step 1 with a w that is not fp8
+ * is FP8_ERR_INVALID_ARG, a bias or need_dbias FP8_ERR_UNSUPPORTED. */
+FP8LIN_API int fp8_linear_grouped_forward(const fp8_linear_fwd_args* args, const fp8_groups* groups,
+                                          fp8_stream_t stream);
+FP8LIN_API int fp8_linear_grouped_backward(const fp8_linear_bwd_args* args, const fp8_groups* groups,
+                                           fp8_stream_t stream);
+
+/* A linear served in 8-bit integers: x [M, K] (bf16/fp16/fp32) is quantized
+ * row by row into x8 and sx_out (fp8_quantize_int8), then y = (x8 w8^T) sx sw +
+ * bias (fp8_mm_int8).  x8 int8 [M, ldx8] and sx_out fp32 [M] are the caller's;
+ * w8 int8 [N, ldw8] and sw fp32 [N] come from fp8_quantize_int8 of the weight.
+ * Two launches.  K = 0: y = bias (or 0), sx_out is left as it was. */
+typedef struct fp8_linear_int8_args {
+  int64_t M, N, K;
+  const void* x; int x_dtype; int64_t ldx;
+  const int8_t* w8; int64_t ldw8; const float* sw;
+  const void* bias; int bias_dtype;
+  int8_t* x8; int64_t ldx8; float* sx_out;
+  void* y; int y_dtype; int64_t ldy;
+} fp8_linear_int8_args;
+FP8LIN_API int fp8_linear_int8_forward(const fp8_linear_int8_args* args, fp8_stream_t stream);
 
 /* Workspace bytes fp8_linear_backward needs for need_dbias (0 when M or N is
  * 0).  Equal to fp8_dbias_workspace_bytes(M, N): one size covers the row
