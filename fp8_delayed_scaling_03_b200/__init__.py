@@ -12,9 +12,9 @@ allocate outputs with torch and call them.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -531,51 +531,121 @@ def linear_backward(g, fwd: ForwardResult, ring_g: ScaleRing | None, fmt_g=FP8_E
 
 
 # --------------------------------------------------------------------------- grouped and int8
+#
+# These helpers run in the microseconds between two small launches, so they
+# look each tensor property up once and hand the argument structs over as
+# packed bytes (half the cost of a ctypes structure).
 
-_FP8_CODES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
-
-
-def _on_device(dev: torch.device, *tensors: torch.Tensor | None):
-    """The operands' device made current for the call (a no-op on the current
-    one); every tensor has to live there."""
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got one on {dev}")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    return torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else contextlib.nullcontext()
+_CODE_TYPES = {torch.uint8: None, torch.float8_e4m3fn: FP8_E4M3, torch.float8_e5m2: FP8_E5M2}
+_WIDE_TYPES = {torch.bfloat16: FP8_DT_BF16, torch.float16: FP8_DT_FP16, torch.float32: FP8_DT_FP32}
 
 
-def _groups(offsets: torch.Tensor, stride_b: int = 0, stride_d: int = 0, scale_b_step: int = 0) -> Groups:
-    if offsets.dim() != 1 or offsets.numel() < 1 or offsets.stride(0) != 1 or \
-            offsets.dtype not in (torch.int32, torch.int64):
-        raise ValueError("offsets: a contiguous int32 or int64 vector of groups + 1 row offsets")
-    return Groups(offsets.numel() - 1, offsets.data_ptr(), int(offsets.dtype == torch.int64), stride_b, stride_d,
-                  scale_b_step)
+def _packer(structure) -> struct.Struct:
+    """A struct.Struct that packs a ctypes structure's fields in order, in its C layout."""
+    letters = {_I64: "q", _I: "i", _P: "P", _SZ: "N"}
+    packer = struct.Struct("@" + "".join(letters[t] for _, t in structure._fields_) + "0q")
+    assert packer.size == ctypes.sizeof(structure)
+    return packer
 
 
-def _expert_matrix(w: torch.Tensor, groups: int, what: str) -> int:
-    """Row stride of a [groups, rows, cols] tensor whose matrices follow one another row by row."""
-    if w.dim() != 3 or w.shape[0] != groups:
-        raise ValueError(f"{what}: expected [groups, rows, columns] with {groups} groups, got {tuple(w.shape)}")
-    if w.shape[2] > 1 and w.stride(2) != 1:
+def _packed_call(name: str, *args):
+    """The entry point `name` with its structs as bytes."""
+    fn = _lib[name]
+    fn.restype, fn.argtypes = _I, args
+    return fn
+
+
+_pack_mm, _pack_groups = _packer(MmArgs).pack, _packer(Groups).pack
+_pack_fwd, _pack_bwd, _pack_int8 = _packer(LinearFwdArgs).pack, _packer(LinearBwdArgs).pack, _packer(LinearInt8Args).pack
+_B = ctypes.c_char_p
+_call_mm_grouped = _packed_call("fp8_mm_grouped", _B, _I, _B, _P)
+_call_grouped_forward = _packed_call("fp8_linear_grouped_forward", _B, _B, _P)
+_call_grouped_backward = _packed_call("fp8_linear_grouped_backward", _B, _B, _P)
+_call_linear_int8 = _packed_call("fp8_linear_int8_forward", _B, _P)
+
+
+def _call(where: str, dev: int, fn, *args) -> None:
+    """fn on the current stream of device `dev`, which is made current for the call."""
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != FP8_OK:
+        raise Fp8Error(status, where)
+
+
+def _one_device(first: torch.Tensor, *others: torch.Tensor | None) -> int:
+    """The index of the GPU all the tensors live on."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"expected CUDA tensors, got one on {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return dev
+
+
+def _address(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, what: str) -> tuple[int, int, int]:
+    """(rows, columns, row stride) of a 2-D tensor with a contiguous last dimension."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what}: expected a 2-D tensor with a contiguous last dimension, got {tuple(shape)}")
+    return shape[0], shape[1], (stride[0] if shape[0] > 1 else max(stride[0], shape[1]))
+
+
+def _experts(t: torch.Tensor, groups: int, what: str) -> tuple[int, int, int]:
+    """(rows, columns, row stride) of each matrix of a [groups, rows, columns] tensor whose matrices follow one another."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != groups:
+        raise ValueError(f"{what}: expected [groups, rows, columns] with {groups} groups, got {tuple(shape)}")
+    if stride[2] != 1 and shape[2] > 1:
         raise ValueError(f"{what}: the last dimension has to be contiguous")
-    ld = w.stride(1)
-    if w.shape[0] > 1 and w.stride(0) != w.shape[1] * ld:
-        raise ValueError(f"{what}: the groups' matrices have to follow one another (stride {w.shape[1] * ld}, "
-                         f"got {w.stride(0)})")
-    return ld
+    if groups > 1 and stride[0] != shape[1] * stride[1]:
+        raise ValueError(f"{what}: the groups' matrices have to follow one another (stride {shape[1] * stride[1]}, "
+                         f"got {stride[0]})")
+    return shape[1], shape[2], stride[1]
+
+
+def _offsets(t: torch.Tensor) -> tuple[int, int]:
+    """(groups, 1 for int64) of a row-offset vector."""
+    shape, dtype = t.shape, t.dtype
+    if len(shape) != 1 or shape[0] < 1 or (t.stride(0) != 1 and shape[0] > 1) or \
+            (dtype != torch.int32 and dtype != torch.int64):
+        raise ValueError("offsets: a contiguous int32 or int64 vector of groups + 1 row offsets")
+    return shape[0] - 1, int(dtype == torch.int64)
 
 
 def _scale_step(scale: torch.Tensor, groups: int, what: str) -> int:
-    if scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() not in (1, groups):
+    n = scale.numel()
+    if scale.dtype != torch.float32 or not scale.is_contiguous() or (n != 1 and n != groups):
         raise ValueError(f"{what}: a contiguous fp32 tensor of 1 or {groups} scales")
-    return int(scale.numel() != 1)
+    return int(n != 1)
 
 
-def _out(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, dev, what: str) -> torch.Tensor:
+def _codes_fmt(t: torch.Tensor, fmt: int, what: str) -> None:
+    """fp8 codes of format fmt: uint8, or the float8 type of that format."""
+    held = _CODE_TYPES.get(t.dtype, -1)
+    if held is not None and held != fmt:
+        raise ValueError(f"{what}: expected fp8 codes of format {fmt}, got {t.dtype}")
+
+
+def _operand_dtype(t: torch.Tensor, fmt: int) -> tuple[int, bool]:
+    """(FP8_DT_*, whether it holds fp8 codes) of a linear's operand."""
+    if t.dtype in _CODE_TYPES:
+        return FP8_DT_E4M3 + (fmt if t.dtype == torch.uint8 else _CODE_TYPES[t.dtype]), True
+    if t.dtype not in _WIDE_TYPES:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return _WIDE_TYPES[t.dtype], False
+
+
+def _out(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, like: torch.Tensor, what: str) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     if tuple(t.shape) != shape or t.dtype != dtype:
         raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     return t
@@ -591,21 +661,25 @@ def grouped_mm(x8, w8, offsets, sx, sw, y=None, fmt_x=FP8_E4M3, fmt_w=FP8_E4M3, 
     """y[r] = x8[r] w8[e]^T / (sx sw[e]) for the rows offsets[e] <= r < offsets[e + 1] (bf16; the other rows of y are
     left as they were, or not initialized).  x8 [rows, k] and w8 [groups, n, k] (w_major FP8_MN_MAJOR: [groups, k, n])
     are fp8 codes, sx one scale, sw one or one per group."""
-    groups = offsets.numel() - 1
-    dev = x8.device
-    (rows, k), ldw = x8.shape, _expert_matrix(w8, groups, "w8")
-    n, kw = (w8.shape[1], w8.shape[2]) if w_major == FP8_K_MAJOR else (w8.shape[2], w8.shape[1])
-    if kw != k or x8.dtype not in _FP8_CODES or w8.dtype not in _FP8_CODES:
-        raise ValueError(f"fp8 codes of one contraction length: got {x8.dtype} {tuple(x8.shape)}, "
-                         f"{w8.dtype} {tuple(w8.shape)}")
-    if sx.numel() != 1:
-        raise ValueError("sx: one scale")
-    g = _groups(offsets, w8.shape[1] * ldw, 0, _scale_step(sw, groups, "sw"))
-    with _on_device(dev, w8, offsets, sx, sw, y):
-        y = _out(y, (rows, n), torch.bfloat16, dev, "y")
-        a = MmArgs(rows, n, k, x8.data_ptr(), fmt_x, FP8_K_MAJOR, _ld(x8), w8.data_ptr(), fmt_w, w_major, ldw,
-                   sx.data_ptr(), sw.data_ptr(), None, 0, None, y.data_ptr(), _ld(y), 0, None, 0)
-        _check(_lib.fp8_mm_grouped(a, FP8_RAGGED_M, g, _stream(dev)), "fp8_mm_grouped")
+    groups, off64 = _offsets(offsets)
+    rows, k, ldx = _matrix(x8, "x8")
+    n, kw, ldw = _experts(w8, groups, "w8")
+    stride = n * ldw
+    if w_major != FP8_K_MAJOR:
+        n, kw = kw, n
+    if kw != k:
+        raise ValueError(f"x8 and w8 of one contraction length: {tuple(x8.shape)}, {tuple(w8.shape)}")
+    _codes_fmt(x8, fmt_x, "x8")
+    _codes_fmt(w8, fmt_w, "w8")
+    if sx.numel() != 1 or sx.dtype != torch.float32:
+        raise ValueError("sx: one fp32 scale")
+    step = _scale_step(sw, groups, "sw")
+    dev = _one_device(x8, w8, offsets, sx, sw, y)
+    y = _out(y, (rows, n), torch.bfloat16, x8, "y")
+    _call("fp8_mm_grouped", dev, _call_mm_grouped,
+          _pack_mm(rows, n, k, x8.data_ptr(), fmt_x, FP8_K_MAJOR, ldx, w8.data_ptr(), fmt_w, w_major, ldw,
+                   sx.data_ptr(), sw.data_ptr(), 0, 0, 0, y.data_ptr(), _matrix(y, "y")[2], FP8_TILE_AUTO, 0, 0),
+          FP8_RAGGED_M, _pack_groups(groups, offsets.data_ptr(), off64, stride, 0, step))
     return y
 
 
@@ -615,40 +689,35 @@ def grouped_linear_forward(x, w, offsets, ring_x: ScaleRing | None, ring_w: Scal
     """y = x w[e]^T for the rows of each group e, through fp8_linear_grouped_forward: the linear_forward of a mixture
     of experts.  x [rows, K] sorted by expert, w [groups, N, K]; either may be bf16/fp16/fp32 or fp8 codes with its
     *_scale_in (w's: one scale, or one per group).  w8 is [groups, N, K]."""
-    groups = offsets.numel() - 1
-    dev = x.device
-    M, K = x.shape
-    ldw = _expert_matrix(w, groups, "w")
-    N = w.shape[1]
-    if w.shape[2] != K:
+    groups, off64 = _offsets(offsets)
+    M, K, ldx = _matrix(x, "x")
+    N, kw, ldw = _experts(w, groups, "w")
+    if kw != K:
         raise ValueError(f"x and w of one contraction length: {tuple(x.shape)}, {tuple(w.shape)}")
-    xq, wq = x.dtype in _FP8_CODES, w.dtype in _FP8_CODES
+    (xd, xq), (wd, wq) = _operand_dtype(x, fmt_x), _operand_dtype(w, fmt_w)
     step = _scale_step(w_scale_in, groups, "w_scale_in") if wq and w_scale_in is not None else 0
-    g = _groups(offsets, 0, 0, step)
-    with _on_device(dev, w, offsets, x_scale_in, w_scale_in, x8, w8, y):
-        y = _out(y, (M, N), torch.bfloat16, dev, "y")
-        if x8 is None:
-            x8 = x.view(torch.uint8) if xq else fp8_alloc(M, K, dev)
-        if w8 is None:
-            w8 = w.view(torch.uint8) if wq else fp8_alloc_experts(groups, N, K, dev)
-        if tuple(x8.shape) != (M, K) or tuple(w8.shape) != (groups, N, K):
-            raise ValueError("x8 [rows, K] and w8 [groups, N, K]")
-        sw_n = groups if step else 1
-        sc = torch.empty(3 + sw_n, dtype=torch.float32, device=dev)
-        sx, amax_x, amax_w, sw = sc[0:1], sc[1:2], sc[2:3], sc[3:]
-        H = ring_x.H if ring_x is not None else (ring_w.H if ring_w is not None else hist_len)
-        args = LinearFwdArgs(
-            M, N, K,
-            _ptr(x), _dtype_code(x, fmt_x), _ld(x), _ptr(x_scale_in),
-            _ptr(w), _dtype_code(w, fmt_w), ldw, _ptr(w_scale_in),
-            None, 0, None,
-            fmt_x, fmt_w, H,
-            _ptr(ring_x.buf) if ring_x is not None else None, _ptr(ring_w.buf) if ring_w is not None else None,
-            _ptr(x8), _ld(x8), _ptr(w8), _expert_matrix(w8, groups, "w8"),
-            _ptr(sx), _ptr(sw), _ptr(amax_x), _ptr(amax_w),
-            _ptr(y), _ld(y))
-        _check(_lib.fp8_linear_grouped_forward(args, g, _stream(dev)), "fp8_linear_grouped_forward")
-    return ForwardResult(y, x8, w8, sx, sw, amax_x, amax_w)
+    ring_x_buf, ring_w_buf = ring_x and ring_x.buf, ring_w and ring_w.buf
+    dev = _one_device(x, w, offsets, x_scale_in, w_scale_in, x8, w8, y, ring_x_buf, ring_w_buf)
+    if ring_x is not None and ring_w is not None and ring_x.H != ring_w.H:
+        raise ValueError("ring_x and ring_w of one history length")
+    H = ring_x.H if ring_x is not None else (ring_w.H if ring_w is not None else hist_len)
+    y = _out(y, (M, N), torch.bfloat16, x, "y")
+    if x8 is None:
+        x8 = x.view(torch.uint8) if xq else fp8_alloc(M, K, x.device)
+    if w8 is None:
+        w8 = w.view(torch.uint8) if wq else fp8_alloc_experts(groups, N, K, x.device)
+    if tuple(x8.shape) != (M, K) or tuple(w8.shape) != (groups, N, K) or x8.dtype != torch.uint8 or \
+            w8.dtype != torch.uint8:
+        raise ValueError("x8 [rows, K] and w8 [groups, N, K] as uint8 codes")
+    sc = x.new_empty(3 + (groups if step else 1), dtype=torch.float32)
+    at = sc.data_ptr()
+    _call("fp8_linear_grouped_forward", dev, _call_grouped_forward,
+          _pack_fwd(M, N, K, x.data_ptr(), xd, ldx, _address(x_scale_in), w.data_ptr(), wd, ldw, _address(w_scale_in),
+                    0, 0, 0, fmt_x, fmt_w, H, _address(ring_x_buf), _address(ring_w_buf),
+                    x8.data_ptr(), _matrix(x8, "x8")[2], w8.data_ptr(), _experts(w8, groups, "w8")[2],
+                    at, at + 12, at + 4, at + 8, y.data_ptr(), _matrix(y, "y")[2]),
+          _pack_groups(groups, offsets.data_ptr(), off64, 0, 0, step))
+    return ForwardResult(y, x8, w8, sc[0:1], sc[3:], sc[1:2], sc[2:3])
 
 
 def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | None, fmt_g=FP8_E5M2, fmt_x=FP8_E4M3,
@@ -656,55 +725,54 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
                             g8=None) -> BackwardResult:
     """dx [rows, K] and dw [groups, N, K] through fp8_linear_grouped_backward, reusing the forward's x8, w8 and scale
     snapshots.  Rows of dx outside every group are left as they were (or not initialized)."""
-    groups = offsets.numel() - 1
-    dev = g.device
-    M, N = g.shape
-    x8, w8 = fwd.x8, fwd.w8
-    K = x8.shape[1]
-    ldw = _expert_matrix(w8, groups, "w8")
-    if x8.shape[0] != M or tuple(w8.shape) != (groups, N, K):
+    groups, off64 = _offsets(offsets)
+    M, N, ldg = _matrix(g, "g")
+    x8, w8, sx, sw = fwd.x8, fwd.w8, fwd.sx, fwd.sw
+    mx, K, ldx8 = _matrix(x8, "x8")
+    nw, kw, ldw8 = _experts(w8, groups, "w8")
+    if mx != M or nw != N or kw != K:
         raise ValueError(f"g {tuple(g.shape)}, x8 {tuple(x8.shape)} and w8 {tuple(w8.shape)} do not fit")
-    gr = _groups(offsets, 0, 0, _scale_step(fwd.sw, groups, "sw"))
-    gq = g.dtype in _FP8_CODES
-    with _on_device(dev, x8, w8, offsets, fwd.sx, fwd.sw, g_scale_in, dx, dw, g8):
-        if g8 is None:
-            g8 = g.view(torch.uint8) if gq else fp8_alloc(M, N, dev)
-        if tuple(g8.shape) != (M, N):
-            raise ValueError("g8 [rows, N]")
-        dx = _out(dx, (M, K), torch.bfloat16, dev, "dx") if need_dx else None
-        dw = _out(dw, (groups, N, K), torch.bfloat16, dev, "dw") if need_dw else None
-        sc = torch.empty(2, dtype=torch.float32, device=dev)
-        args = LinearBwdArgs(
-            M, N, K,
-            _ptr(g), _dtype_code(g, fmt_g), _ld(g), _ptr(g_scale_in),
-            fmt_g, ring_g.H if ring_g is not None else 16, _ptr(ring_g.buf) if ring_g is not None else None,
-            _ptr(g8), _ld(g8), _ptr(sc[0:1]), _ptr(sc[1:2]),
-            _ptr(x8), _ld(x8), _ptr(fwd.sx), fmt_x,
-            _ptr(w8), ldw, _ptr(fwd.sw), fmt_w,
-            int(need_dx), int(need_dw), 0,
-            _ptr(dx), _ld(dx) if need_dx else 0,
-            _ptr(dw), _expert_matrix(dw, groups, "dw") if need_dw else 0,
-            None, None, 0)
-        _check(_lib.fp8_linear_grouped_backward(args, gr, _stream(dev)), "fp8_linear_grouped_backward")
+    _codes_fmt(x8, fmt_x, "x8")
+    _codes_fmt(w8, fmt_w, "w8")
+    if sx.numel() != 1 or sx.dtype != torch.float32:
+        raise ValueError("sx: one fp32 scale")
+    step = _scale_step(sw, groups, "sw")
+    gd, gq = _operand_dtype(g, fmt_g)
+    ring_buf = ring_g and ring_g.buf
+    dev = _one_device(g, x8, w8, offsets, sx, sw, g_scale_in, dx, dw, g8, ring_buf)
+    if g8 is None:
+        g8 = g.view(torch.uint8) if gq else fp8_alloc(M, N, g.device)
+    if tuple(g8.shape) != (M, N) or g8.dtype != torch.uint8:
+        raise ValueError("g8 [rows, N] as uint8 codes")
+    dx = _out(dx, (M, K), torch.bfloat16, g, "dx") if need_dx else None
+    dw = _out(dw, (groups, N, K), torch.bfloat16, g, "dw") if need_dw else None
+    sc = g.new_empty(2, dtype=torch.float32)
+    at = sc.data_ptr()
+    _call("fp8_linear_grouped_backward", dev, _call_grouped_backward,
+          _pack_bwd(M, N, K, g.data_ptr(), gd, ldg, _address(g_scale_in), fmt_g, ring_g.H if ring_g is not None else 16,
+                    _address(ring_buf), g8.data_ptr(), _matrix(g8, "g8")[2], at, at + 4,
+                    x8.data_ptr(), ldx8, sx.data_ptr(), fmt_x, w8.data_ptr(), ldw8, sw.data_ptr(), fmt_w,
+                    int(need_dx), int(need_dw), 0, _address(dx), _matrix(dx, "dx")[2] if need_dx else 0,
+                    _address(dw), _experts(dw, groups, "dw")[2] if need_dw else 0, 0, 0, 0),
+          _pack_groups(groups, offsets.data_ptr(), off64, 0, 0, step))
     return BackwardResult(dx, dw, None, g8, sc[0:1], sc[1:2])
-
-
-def int8_alloc(rows: int, cols: int, device) -> torch.Tensor:
-    """int8 code buffer [rows, ld] with ld = cols rounded up to 16, returned as the [rows, cols] view."""
-    return fp8_alloc(rows, cols, device).view(torch.int8)
 
 
 def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None):
     """Rows of x to int8 by their own largest magnitude; returns (codes [rows, cols], scale [rows] fp32).  A weight
     [N, K] quantized so has one scale per output channel."""
-    dev = x.device
-    rows, cols = x.shape
-    with _on_device(dev, out, scale):
-        out = int8_alloc(rows, cols, dev) if out is None else _out(out, (rows, cols), torch.int8, dev, "out")
-        scale = _out(scale, (rows,), torch.float32, dev, "scale")
-        if not scale.is_contiguous():
-            raise ValueError("scale: contiguous")
-        fp8_quantize_int8(x, out, scale)
+    rows, cols, ldx = _matrix(x, "x")
+    if x.dtype not in _WIDE_TYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    dev = _one_device(x, out, scale)
+    if out is None:  # the kernel writes a row's padding too
+        out = x.new_empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8)[:, :cols]
+    out = _out(out, (rows, cols), torch.int8, x, "out")
+    scale = _out(scale, (rows,), torch.float32, x, "scale")
+    if not scale.is_contiguous():
+        raise ValueError("scale: contiguous")
+    _call("fp8_quantize_int8", dev, _lib.fp8_quantize_int8, x.data_ptr(), _WIDE_TYPES[x.dtype], rows, cols, ldx,
+          out.data_ptr(), _matrix(out, "out")[2], scale.data_ptr())
     return out, scale
 
 
@@ -719,23 +787,32 @@ def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) 
     """y = x w^T + bias in 8-bit integers through fp8_linear_int8_forward: x [rows, K] (bf16/fp16/fp32) is quantized
     row by row, w8 [N, K] int8 and sw [N] come from quantize_int8.  y has x's type unless out_dtype (or y) says
     otherwise."""
-    dev = x.device
-    (M, K), N = x.shape, w8.shape[0]
-    if w8.dim() != 2 or w8.shape[1] != K or w8.dtype != torch.int8:
+    M, K, ldx = _matrix(x, "x")
+    N, kw, ldw = _matrix(w8, "w8")
+    if kw != K or w8.dtype != torch.int8:
         raise ValueError(f"w8: int8 [N, {K}], got {w8.dtype} {tuple(w8.shape)}")
     if sw.dtype != torch.float32 or sw.numel() != N or not sw.is_contiguous():
         raise ValueError(f"sw: {N} contiguous fp32 scales")
     if bias is not None and (bias.numel() != N or not bias.is_contiguous()):
         raise ValueError(f"bias: {N} contiguous values")
-    with _on_device(dev, w8, sw, bias, y, x8, sx):
-        y = _out(y, (M, N), out_dtype or (y.dtype if y is not None else x.dtype), dev, "y")
-        if x8 is None:
-            x8 = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :K]
-        sx = _out(sx, (M,), torch.float32, dev, "sx")
-        if tuple(x8.shape) != (M, K) or x8.dtype != torch.int8 or not sx.is_contiguous():
-            raise ValueError("x8 int8 [rows, K], sx contiguous")
-        args = LinearInt8Args(M, N, K, x.data_ptr(), _dtype_code(x), _ld(x), w8.data_ptr(), _ld(w8), sw.data_ptr(),
-                              _ptr(bias), _dtype_code(bias) if bias is not None else 0,
-                              x8.data_ptr(), _ld(x8), sx.data_ptr(), y.data_ptr(), _dtype_code(y), _ld(y))
-        _check(_lib.fp8_linear_int8_forward(args, _stream(dev)), "fp8_linear_int8_forward")
+    out_dtype = out_dtype or (y.dtype if y is not None else x.dtype)
+    for t in (x.dtype, out_dtype) if bias is None else (x.dtype, out_dtype, bias.dtype):
+        if t not in _WIDE_TYPES:
+            raise TypeError(f"unsupported dtype {t}")
+    dev = _one_device(x, w8, sw, bias, y, x8, sx)
+    y = _out(y, (M, N), out_dtype, x, "y")
+    if x8 is None:
+        ld = (K + 15) // 16 * 16
+        x8 = x.new_empty((M, ld), dtype=torch.int8)
+        if ld != K:
+            x8 = x8[:, :K]
+    elif tuple(x8.shape) != (M, K) or x8.dtype != torch.int8:
+        raise ValueError("x8: int8 [rows, K]")
+    sx = _out(sx, (M,), torch.float32, x, "sx")
+    if not sx.is_contiguous():
+        raise ValueError("sx: contiguous")
+    _call("fp8_linear_int8_forward", dev, _call_linear_int8,
+          _pack_int8(M, N, K, x.data_ptr(), _WIDE_TYPES[x.dtype], ldx, w8.data_ptr(), ldw, sw.data_ptr(),
+                     _address(bias), 0 if bias is None else _WIDE_TYPES[bias.dtype], x8.data_ptr(),
+                     _matrix(x8, "x8")[2], sx.data_ptr(), y.data_ptr(), _WIDE_TYPES[out_dtype], _matrix(y, "y")[2]))
     return Int8Result(y, x8, sx)

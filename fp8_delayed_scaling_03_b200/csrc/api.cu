@@ -746,10 +746,25 @@ struct GroupedCall {
 };
 
 // An upper bound on a launch's tiles: every group may waste one partial tile.
-int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile) {
-  const int64_t tl = (c.nlane + 127) / 128;
+int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile, int64_t tile_lanes = 128) {
+  const int64_t tl = (c.nlane + tile_lanes - 1) / tile_lanes;
   if (c.ragged_k) return tl * ((c.ncol + col_tile - 1) / col_tile) * c.groups;
   return tl * (c.rows / col_tile + std::min(c.groups, c.rows));
+}
+
+// Tiles of a launch: pairs (256 lanes x 256 columns) where there is enough
+// work to fill the pairs of SMs with them, else one CTA per tile.
+void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair) {
+  const int64_t tl2 = (c.nlane + 255) / 256;
+  if (c.ragged_k) {
+    *pair = tl2 * ((c.ncol + 255) / 256) * c.groups >= sms / 2;
+    *tile = *pair ? 256 : 128;
+    return;
+  }
+  const int64_t live = std::max<int64_t>(1, std::min(c.groups, c.rows));
+  const int64_t avg = (c.rows + live - 1) / live;
+  *pair = avg > 128 && (avg + 255) / 256 * live * tl2 >= sms / 2;
+  *tile = *pair ? 256 : pick_col_tile(c.rows, c.groups, (c.nlane + 127) / 128, sms);
 }
 
 // One launch of a validated call with at least one group and lane.
@@ -761,13 +776,14 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   if (e != cudaSuccess) return cuda_fail(e);
   const int sms = num_sms(dev);
   if (sms <= 0 || dev >= 64) return cuda_fail(cudaGetLastError());
-  const int64_t tl = (c.nlane + 127) / 128;
   int tile;
-  if (c.ragged_k) tile = tl * ((c.ncol + 255) / 256) * c.groups >= sms ? 256 : 128;
-  else tile = pick_col_tile(c.rows, c.groups, tl, sms);
+  bool pair;
+  pick_grouped_tile(c, sms, &tile, &pair);
+  const int tile_lanes = pair ? 256 : 128;
+  const int64_t tl = (c.nlane + tile_lanes - 1) / tile_lanes;
   GroupedParams p;
   std::memset(&p, 0, sizeof(p));
-  CUtensorMap maps[3];
+  CUtensorMap maps[4];
   std::memset(maps, 0, sizeof(maps));
   int s;
   if (c.ragged_k) {
@@ -781,8 +797,9 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
     s = c.lane_mn ? make_fp8_map(&maps[0], c.lane_op, c.nlane, c.k, c.ld_lane, 128, batch, c.stride_lane)
                   : make_fp8_map(&maps[0], c.lane_op, c.k, c.nlane, c.ld_lane, 128, batch, c.stride_lane);
     if (s) return s;
-    if ((s = make_fp8_map(&maps[1], c.col_op, c.k, c.rows, c.ld_col, static_cast<uint32_t>(tile)))) return s;
-    if ((s = make_fp8_map(&maps[2], c.col_op, c.k, c.rows, c.ld_col, 32))) return s;
+    if ((s = make_fp8_map(&maps[1], c.col_op, c.k, c.rows, c.ld_col, static_cast<uint32_t>(pair ? tile / 2 : tile)))) return s;
+    // (a tile of at most 32 rows is always one whole copy)
+    if (tile > 32 && (s = make_fp8_map(&maps[2], c.col_op, c.k, c.rows, c.ld_col, 32))) return s;
   }
   p.groups = static_cast<int>(c.groups);
   p.rows = static_cast<int>(c.rows);
@@ -795,9 +812,10 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   p.k_blocks = static_cast<int>(((c.ragged_k ? c.rows : c.k) + 127) / 128);
   p.lane_shared = c.stride_lane == 0 ? 1 : 0;
   p.col_tile = tile;
-  p.stages = grouped_stages(tile);
+  grouped_smem(&p, pair);
   p.lane_mn = c.lane_mn;
-  p.idesc = c.int8 ? idesc_i8(128, 0) : idesc_f8(c.fmt_lane, c.fmt_col, c.lane_mn, c.ragged_k ? 1 : 0, 128, 0);
+  p.idesc = c.int8 ? idesc_i8(tile_lanes, 0)
+                     : idesc_f8(c.fmt_lane, c.fmt_col, c.lane_mn, c.ragged_k ? 1 : 0, tile_lanes, 0);
   p.scale_a = c.scale_a;
   p.scale_b = c.scale_b;
   p.scale_b_step = c.scale_b_step;
@@ -807,6 +825,17 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   p.ldd = c.ldd;
   p.stride_d = c.ragged_k ? c.stride_d : 0;
   p.vec_ok = aligned(c.d, 16) && (c.ldd * 2) % 16 == 0 && (p.stride_d * 2) % 16 == 0;
+  // whole 2-byte blocks through TMA, as in build_problem; a launch whose tiles
+  // are smaller than a block has none
+  p.tma_store = p.vec_ok && c.nlane % 8 == 0 && esize(c.d_dtype) == 2 && tile >= 32;
+  if (p.tma_store) {
+    s = c.ragged_k ? make_map(&maps[3], c.d, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.nlane, c.ncol, c.ldd * 2, 32, 32,
+                              CU_TENSOR_MAP_SWIZZLE_64B, static_cast<uint64_t>(c.groups),
+                              static_cast<uint64_t>(c.stride_d) * 2)
+                   : make_map(&maps[3], c.d, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.nlane, c.rows, c.ldd * 2, 32, 32,
+                              CU_TENSOR_MAP_SWIZZLE_64B);
+    if (s) return s;
+  }
   p.status = status_ptr(dev);
   if (side) p.side = *side;
   for (int i = 0; i < nfin; ++i) p.fin[i] = fin[i];
@@ -814,7 +843,7 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   p.sw_src = sw_src;
   p.sw_dst = sw_dst;
   p.sw_n = sw_n;
-  e = launch_grouped(maps, p, c.int8, c.ragged_k, c.d_dtype, grouped_max_tiles(c, tile), st);
+  e = launch_grouped(maps, p, c.int8, c.ragged_k, pair, c.d_dtype, grouped_max_tiles(c, tile, tile_lanes), st);
   return e == cudaSuccess ? FP8_OK : cuda_fail(e);
 }
 

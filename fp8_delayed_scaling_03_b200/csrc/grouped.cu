@@ -27,12 +27,16 @@
 //     group's end.  Whole 32-row steps past it are not issued; the rows of
 //     the last step past it are set to zero in both operands' shared memory
 //     (in both, since an fp8 NaN of the next group times zero would be NaN).
+// The stages of the operand ring take what shared memory the group tables (8
+// bytes a group) leave: 192 KB up to 190 groups, a stage less beyond.
 // Roles as in gemm.cu: warp 0 lane 0 TMA producer, warp 1 MMA issuer, warps
 // 2-9 epilogue over double-buffered TMEM accumulators, every wait bounded.
 // The epilogue reads 16 lanes x 32 columns per tcgen05.ld.16x256b, whose
 // register layout is the one stmatrix takes: stmatrix.trans turns the block
-// over so that a token's 32 outputs are 64 contiguous bytes, which leave as
-// 16-byte stores guarded by the group's end.
+// over so that a token's 32 outputs are 64 contiguous bytes in a swizzled slab,
+// which leaves by a TMA store.  A block cut by its group's end (which TMA
+// cannot clip: the next group's rows follow) leaves as 16-byte stores guarded
+// by that end, and one of rows that TMA cannot address as single elements.
 #include <algorithm>
 
 #include "device.cuh"
@@ -49,15 +53,17 @@ constexpr int kStep = 32;                // contraction per MMA
 constexpr int kThreads = 320;            // 10 warps: TMA, MMA, 8 epilogue
 constexpr int kEpiWarps = 8;
 constexpr int kSlab = 32 * 32 * 2;       // one staged 32 x 32 block of 2-byte outputs
+constexpr int kSlabBytes = kEpiWarps * 2 * kSlab;  // two per epilogue warp
 constexpr int kLaneBytes = kLanes * kKBlock;
 constexpr int kOperandBytes = 192 * 1024;
 constexpr int kMaxStages = 10;
-constexpr int kBarBytes = 256;
+constexpr int kBarBytes = 512;
 constexpr int kTmemCols = 512;           // two accumulators of up to 256 columns
 constexpr int kRaster = 8;               // token tiles per raster group
-constexpr int kSmem = kOperandBytes + kEpiWarps * kSlab + kBarBytes + 2 * (kMaxGroups + 1) * 4 + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-static_assert((2 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barrier block");
+// Shared memory: [operand stages][slabs][barriers][group bounds, first tiles].
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kFixedSmem = 1024 + kSlabBytes + kBarBytes;
+static_assert((3 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barrier block");
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -88,6 +94,54 @@ __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on an mbarrier of either CTA of the pair without release: it tells
+// that TMEM reads have completed (tcgen05.wait::ld before it), no memory is
+// handed over.  A release at cluster scope would wait for the warp's output
+// stores to be performed first.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Order this thread's generic-proxy writes of its shared memory before
+// async-proxy reads of them by either CTA of the pair.
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
+
 template <int OUT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (OUT == kFP16) {
@@ -106,12 +160,13 @@ __device__ __forceinline__ float load_bias(const void* bias, int dtype, int j) {
 }
 
 // One tile: `cols` output rows from col0 (rows of the buffer, or of D_e for
-// dW) by 128 lanes from lane0, contraction blocks [0, kb) from row/byte k0.
+// dW) by 128 (a pair's: 256) lanes from lane0, contraction blocks [0, kb) from
+// row/byte k0; kvalid rows of the group remain from k0 (dW).
 struct Tile {
   int e, col0, cols, lane0, kb, k0, kvalid;
 };
 
-template <bool kRaggedK>
+template <bool kRaggedK, int kTileLanes>
 __device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* bound, const int* first, int t) {
   Tile w;
   if constexpr (kRaggedK) {
@@ -119,7 +174,7 @@ __device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* bound
     w.e = t / per;
     t -= w.e * per;
     const int tl = t % p.tiles_lane, tc = t / p.tiles_lane;
-    w.lane0 = tl * kLanes;
+    w.lane0 = tl * kTileLanes;
     w.col0 = tc * p.col_tile;
     w.cols = min(p.col_tile, p.ncol - w.col0);
     w.k0 = bound[w.e];
@@ -142,7 +197,7 @@ __device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* bound
     const int gc = min(kRaster, tiles_col - g * kRaster);
     t -= g * per;
     const int tc = g * kRaster + t % gc;
-    w.lane0 = (t / gc) * kLanes;
+    w.lane0 = (t / gc) * kTileLanes;
     w.col0 = row0 + tc * p.col_tile;
     w.cols = min(p.col_tile, row0 + rows - w.col0);
     w.k0 = 0;
@@ -205,58 +260,88 @@ __device__ __forceinline__ void scan_groups(const GroupedParams& p, int* bound, 
   }
 }
 
+// Clears rows [from, to) of this CTA's `chunks` operand chunks of 128 rows x
+// 128 bytes (MN-major: a row is one index of the contraction).  One warp.
+__device__ __forceinline__ void clear_rows(uint8_t* stage, int chunks, int from, int to, int lane) {
+  const int words = (to - from) * (kKBlock / 16);
+  for (int c = 0; c < chunks; ++c) {
+    uint4* row = reinterpret_cast<uint4*>(stage + c * 128 * kKBlock + from * kKBlock);
+    for (int i = lane; i < words; i += 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // kInt8: 8-bit integer operands with row and lane scales; else fp8 with one
 // scale per tensor or group.  kRaggedK: the contraction is ragged (dW).
-template <bool kInt8, bool kRaggedK, int OUT>
+// kPair: a cluster of two CTAs runs tiles of 256 lanes with 2-SM MMAs: each CTA
+// loads 128 lanes and half of the columns into its own shared memory, the even
+// one issues, and each holds its 128 lanes' accumulators.
+template <bool kInt8, bool kRaggedK, bool kPair, int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap t_lane, const __grid_constant__ CUtensorMap t_col,
-                   const __grid_constant__ CUtensorMap t_col32, const __grid_constant__ GroupedParams p) {
+                   const __grid_constant__ CUtensorMap t_col32, const __grid_constant__ CUtensorMap t_d,
+                   const __grid_constant__ GroupedParams p) {
+  constexpr int kTileLanes = kPair ? 2 * kLanes : kLanes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int col_bytes = max(p.col_tile, 32) * kKBlock;   // a 16-column tile keeps 32-row slots: 1024-byte aligned stages
+  const int cta_cols = kPair ? p.col_tile / 2 : p.col_tile;   // columns of a whole tile that this CTA loads
+  const int col_bytes = max(cta_cols, 32) * kKBlock;   // a 16-column tile keeps 32-row slots: 1024-byte aligned stages
   const int stage_bytes = kLaneBytes + col_bytes;
-  uint8_t* s_epi = smem + kOperandBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + kEpiWarps * kSlab);
+  uint8_t* s_epi = smem + p.stages * stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_epi + kSlabBytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  // pair, dW, one per stage: in the odd CTA its part of a group's last block
+  // landed (bytes); in the even CTA the odd one's part is cleared
+  uint64_t* tail = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + kMaxStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* bound = reinterpret_cast<int*>(s_epi + kEpiWarps * kSlab + kBarBytes);
-  int* first = bound + kMaxGroups + 1;
+  int* bound = reinterpret_cast<int*>(s_epi + kSlabBytes + kBarBytes);
+  int* first = bound + p.groups + 1;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nstages = p.stages;
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
+  const int unit = kPair ? static_cast<int>(blockIdx.x) >> 1 : static_cast<int>(blockIdx.x);
+  const int units = kPair ? static_cast<int>(gridDim.x) >> 1 : static_cast<int>(gridDim.x);
 
   if (threadIdx.x == 64) {
     for (int s = 0; s < nstages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      if (kRaggedK && kPair) mbar_init(&tail[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], kEpiWarps);
+      mbar_init(&tempty[a], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (p.tma_store) prefetch_tmap(&t_d);
     if (p.k_blocks > 0) {  // an empty contraction has no maps
       prefetch_tmap(&t_lane);
       prefetch_tmap(&t_col);
-      if (!kRaggedK) prefetch_tmap(&t_col32);
+      if (!kRaggedK && p.col_tile > 32) prefetch_tmap(&t_col32);
     }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
   }
   // Offsets, operands and scales may be the previous kernel's output.
   pdl_wait();
   if (warp == 3) scan_groups<kRaggedK>(p, bound, first, lane);
   tc_fence_before();
-  cta_sync();
+  if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist before either signals the other
+  else cta_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int tiles = first[p.groups];
@@ -264,113 +349,229 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int t = blockIdx.x; t < tiles && !*abort_flag; t += gridDim.x) {
-        const Tile w = tile_of<kRaggedK>(p, bound, first, t);
-        // columns loaded: the whole tile in one copy, or as many 32-row
-        // copies as hold the group's remaining tokens
-        const bool whole = kRaggedK || w.cols > p.col_tile - 32 || p.col_tile <= 32;
-        const int boxes = kRaggedK ? (w.cols + 127) / 128 : (whole ? 1 : (w.cols + 31) / 32);
-        const int bytes = kLaneBytes + (kRaggedK ? boxes * 128 * kKBlock : (whole ? p.col_tile : boxes * 32) * kKBlock);
-        const int z = kRaggedK || p.lane_shared ? 0 : w.e;
-        for (int kb = 0; kb < w.kb; ++kb, ++issued) {
-          if (issued >= nstages && !mbar_wait(&empty[stage], phase ^ 1u, p.status, abort_flag)) break;
-          uint8_t* s_lane = smem + stage * stage_bytes;
-          uint8_t* s_col = s_lane + kLaneBytes;
-          const int k = w.k0 + kb * kKBlock;
-          mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(bytes));
-          if (p.lane_mn) tma_load_3d(s_lane, &t_lane, &full[stage], w.lane0, k, z);
-          else           tma_load_3d(s_lane, &t_lane, &full[stage], k, w.lane0, z);
+    // (the whole warp, converged, one elected lane issues: see the MMA issuer)
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int t = unit; t < tiles; t += units) {
+      const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+      // columns this CTA loads: its whole share of the tile in one copy, or
+      // as many 32-row copies as hold its share of the remaining tokens
+      const int share = kPair ? (w.cols + 31) / 32 * 16 : w.cols;
+      const bool whole = kRaggedK || share > cta_cols - 32 || cta_cols <= 32;
+      const int boxes = kRaggedK ? (kPair ? 1 : (w.cols + 127) / 128) : (whole ? 1 : (share + 31) / 32);
+      const int bytes = kLaneBytes + (kRaggedK ? boxes * 128 : (whole ? cta_cols : boxes * 32)) * kKBlock;
+      const int lane0 = w.lane0 + rank * kLanes;
+      const int col0 = w.col0 + rank * (kRaggedK ? 128 : share);
+      const int z = kRaggedK || p.lane_shared ? 0 : w.e;
+      auto load = [&](int st, int kb) {
+        uint8_t* s_lane = smem + st * stage_bytes;
+        uint8_t* s_col = s_lane + kLaneBytes;
+        const int k = w.k0 + kb * kKBlock;
+        const int lane_x = p.lane_mn ? lane0 : k, lane_y = p.lane_mn ? k : lane0;
+        if constexpr (kPair) {
+          // Both CTAs' bytes are counted on the even CTA's full barrier -- but
+          // for a block whose last rows have to be cleared: there the odd CTA's
+          // bytes go to its own tail barrier, for the warp that clears.
+          const bool clear = kRaggedK && kb == w.kb - 1 && w.kvalid % kStep != 0;
+          uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+          if (rank == 0) {
+            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(clear ? bytes : 2 * bytes));
+          } else if (clear) {
+            bar = mapa_shared(smem_u32(&tail[st]), 1);
+            mbar_arrive_expect_tx(&tail[st], static_cast<uint32_t>(bytes));
+          }
+          tma_load_3d_pair(s_lane, &t_lane, bar, lane_x, lane_y, z);
           if constexpr (kRaggedK) {
-            for (int b = 0; b < boxes; ++b)
-              tma_load_3d(s_col + b * 128 * kKBlock, &t_col, &full[stage], w.col0 + b * 128, k, 0);
+            tma_load_3d_pair(s_col, &t_col, bar, col0, k, 0);
           } else if (whole) {
-            tma_load_3d(s_col, &t_col, &full[stage], k, w.col0, 0);
+            tma_load_3d_pair(s_col, &t_col, bar, k, col0, 0);
           } else {
             for (int b = 0; b < boxes; ++b)
-              tma_load_3d(s_col + b * 32 * kKBlock, &t_col32, &full[stage], k, w.col0 + b * 32, 0);
+              tma_load_3d_pair(s_col + b * 32 * kKBlock, &t_col32, bar, k, col0 + b * 32, 0);
           }
-          if (++stage == nstages) { stage = 0; phase ^= 1u; }
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // dW runs the loop with the whole warp (its lanes clear the rows past a
-    // group's end), lane 0 alone waits and issues; else lane 0 only.
-    if (kRaggedK || lane == 0) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true, issued = false;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile w = tile_of<kRaggedK>(p, bound, first, t);
-        // N: the tile's columns, rounded up to 16; dW's column operand is
-        // MN-major in chunks of 128, which it takes whole
-        const int n = kRaggedK ? (w.cols + 127) / 128 * 128 : (w.cols + 15) / 16 * 16;
-        const uint32_t idesc = p.idesc | static_cast<uint32_t>(n >> 3) << 17;
-        if (lane == 0) ok = mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag);
-        if (kRaggedK) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-        for (int kb = 0; kb < w.kb; ++kb) {
-          if (lane == 0) ok = mbar_wait(&full[stage], phase, p.status, abort_flag);
-          if (kRaggedK) ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-          if (!ok) break;
-          tc_fence_after();
-          uint8_t* s_lane = smem + stage * stage_bytes;
-          int steps = kKBlock / kStep;
+        } else {
+          mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(bytes));
+          tma_load_3d(s_lane, &t_lane, &full[st], lane_x, lane_y, z);
           if constexpr (kRaggedK) {
-            const int valid = w.kvalid - kb * kKBlock;   // rows of this block inside the group
-            if (valid < kKBlock) {
-              steps = (valid + kStep - 1) / kStep;
-              if (valid % kStep) {
-                (void)mbar_try_wait(smem_u32(&full[stage]), phase);  // each lane acquires the copies' bytes
-                // rows [valid, 32 steps) of the lane operand and of each 128-column chunk of the other:
-                // 128 bytes a row, 16 per lane
-                const int chunks = 1 + (w.cols + 127) / 128;
-                const int words = (steps * kStep - valid) * (kKBlock / 16);
-                for (int c = 0; c < chunks; ++c) {
-                  uint4* row = reinterpret_cast<uint4*>(s_lane + c * 128 * kKBlock + valid * kKBlock);
-                  for (int i = lane; i < words; i += 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+            for (int b = 0; b < boxes; ++b)
+              tma_load_3d(s_col + b * 128 * kKBlock, &t_col, &full[st], col0 + b * 128, k, 0);
+          } else if (whole) {
+            tma_load_3d(s_col, &t_col, &full[st], k, col0, 0);
+          } else {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_3d(s_col + b * 32 * kKBlock, &t_col32, &full[st], k, col0 + b * 32, 0);
+          }
+        }
+      };
+      bool ok = true;
+      int kb = 0;
+      while (kb < w.kb) {
+        // two blocks at a time where both stages are free (the first nstages
+        // loads find them so)
+        const bool wrap = stage + 1 == nstages;
+        const int stage1 = wrap ? 0 : stage + 1;
+        const uint32_t phase1 = wrap ? phase ^ 1u : phase;
+        const bool second = kb + 1 < w.kb && (issued + 1 < nstages || mbar_test(&empty[stage1], phase1 ^ 1u));
+        ok = __all_sync(0xFFFFFFFFu, issued < nstages || mbar_wait(&empty[stage], phase ^ 1u, p.status, abort_flag));
+        if (!ok) break;
+        const bool two = __all_sync(0xFFFFFFFFu, second);
+        if (elect_one()) {
+          load(stage, kb);
+          if (two) load(stage1, kb + 1);
+        }
+        __syncwarp();
+        issued = min(issued + (two ? 2 : 1), nstages);
+        kb += two ? 2 : 1;
+        stage = two ? stage1 : stage;
+        phase = two ? phase1 : phase;
+        if (++stage == nstages) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop, converged, so that descriptors and loop
+    // state stay in uniform registers; one elected lane issues.  (With lane 0
+    // alone in the loop a k-block of four MMAs took 0.33 us to issue whatever
+    // its columns, about as long as 256 columns take to compute.)  The lanes
+    // also clear the rows past a group's end for dW.
+    const uint32_t step_k = p.lane_mn ? kStep * 128 >> 4 : kStep >> 4;   // descriptor units per 32 of the contraction
+    constexpr uint32_t kColStep = kRaggedK ? kStep * 128 >> 4 : kStep >> 4;
+    const uint32_t smem_base = smem_u32(smem);
+    const uint64_t a_desc = p.lane_mn ? smem_desc_sw128(smem_base, 128 * kKBlock, 1024) : smem_desc_sw128(smem_base, 16, 1024);
+    const uint64_t b_desc = kRaggedK ? smem_desc_sw128(smem_base + kLaneBytes, 128 * kKBlock, 1024)
+                                     : smem_desc_sw128(smem_base + kLaneBytes, 16, 1024);
+    const uint32_t stage_units = static_cast<uint32_t>(stage_bytes) >> 4;
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    uint32_t tail_phases = 0;   // one bit per stage
+    bool ok = true, issued = false;
+    // the next tile is looked up while the current one's first MMAs run, so
+    // that the search is not in the way between two tiles
+    Tile w{}, next{};
+    if (unit < tiles) next = tile_of<kRaggedK, kTileLanes>(p, bound, first, unit);
+    for (int t = unit; t < tiles && ok; t += units) {
+      w = next;
+      if (w.kb == 0 && t + units < tiles) next = tile_of<kRaggedK, kTileLanes>(p, bound, first, t + units);
+      // N: the tile's columns, rounded up to 16 (a pair's: 32); dW's column
+      // operand is MN-major in chunks of 128, which it takes whole
+      const int n = kRaggedK ? (kPair ? 256 : (w.cols + 127) / 128 * 128)
+                             : (kPair ? (w.cols + 31) / 32 * 32 : (w.cols + 15) / 16 * 16);
+      const uint32_t idesc = p.idesc | static_cast<uint32_t>(n >> 3) << 17;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+      // the MMAs of one k-block and the commit that frees its stage; one lane
+      auto issue = [&](int st, int kb, int steps) {
+        const uint64_t ad = a_desc + static_cast<uint32_t>(st) * stage_units;
+        const uint64_t bd = b_desc + static_cast<uint32_t>(st) * stage_units;
+        #pragma unroll
+        for (int kk = 0; kk < kKBlock / kStep; ++kk) {
+          if (kRaggedK && kk >= steps) break;
+          const uint32_t accum = (kb | kk) ? 1u : 0u;
+          if constexpr (kInt8) {
+            if constexpr (kPair) umma_i8_pair(d_tmem, ad + kk * step_k, bd + kk * kColStep, idesc, accum);
+            else                 umma_i8(d_tmem, ad + kk * step_k, bd + kk * kColStep, idesc, accum);
+          } else {
+            if constexpr (kPair) umma_f8f6f4_pair(d_tmem, ad + kk * step_k, bd + kk * kColStep, idesc, accum);
+            else                 umma_f8f6f4(d_tmem, ad + kk * step_k, bd + kk * kColStep, idesc, accum);
+          }
+        }
+        if constexpr (kPair) {
+          const uint32_t e = smem_u32(&empty[st]);
+          umma_commit_pair(e);
+          umma_commit_pair(mapa_shared(e, 1));
+        } else {
+          umma_commit(&empty[st]);
+        }
+      };
+      int kb = 0;
+      while (kb < w.kb) {
+        // Two blocks at a time where the second has landed too: waits, fences
+        // and elections cost more issue time than the four MMAs between them.
+        const int whole = kRaggedK ? w.kvalid / kKBlock : w.kb;   // blocks that need no clearing
+        const bool wrap = stage + 1 == nstages;
+        const int stage1 = wrap ? 0 : stage + 1;
+        const uint32_t phase1 = wrap ? phase ^ 1u : phase;
+        const bool second = kb + 1 < whole && mbar_test(&full[stage1], phase1);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, p.status, abort_flag));
+        if (!ok) break;
+        const bool two = __all_sync(0xFFFFFFFFu, second);
+        int steps = kKBlock / kStep;
+        if constexpr (kRaggedK) {
+          if (kb >= whole) {   // the last block runs past the group's end
+            const int valid = w.kvalid - kb * kKBlock;
+            steps = (valid + kStep - 1) / kStep;
+            if (valid % kStep) {
+              clear_rows(smem + stage * stage_bytes, kPair ? 2 : 1 + (w.cols + 127) / 128, valid, steps * kStep, lane);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if constexpr (kPair) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tail[stage], (tail_phases >> stage) & 1u, p.status, abort_flag));
+                if (!ok) break;
+                tail_phases ^= 1u << stage;
               }
             }
           }
-          if (lane == 0) {
-            const uint32_t a_base = smem_u32(s_lane), b_base = a_base + kLaneBytes;
-            #pragma unroll
-            for (int kk = 0; kk < kKBlock / kStep; ++kk) {
-              if (kRaggedK && kk >= steps) break;
-              // K-major: 32 bytes along the swizzled 128-byte row; MN-major: 32 rows of 128 bytes
-              const uint64_t ad = !p.lane_mn ? smem_desc_sw128(a_base + kk * kStep, 16, 1024)
-                                             : smem_desc_sw128(a_base + kk * kStep * 128, 128 * kKBlock, 1024);
-              const uint64_t bd = !kRaggedK ? smem_desc_sw128(b_base + kk * kStep, 16, 1024)
-                                            : smem_desc_sw128(b_base + kk * kStep * 128, 128 * kKBlock, 1024);
-              const uint32_t accum = (kb | kk) ? 1u : 0u;
-              if constexpr (kInt8) umma_i8(d_tmem, ad, bd, idesc, accum);
-              else                 umma_f8f6f4(d_tmem, ad, bd, idesc, accum);
-            }
-            umma_commit(&empty[stage]);
-          }
-          if (kRaggedK) __syncwarp();
-          if (++stage == nstages) { stage = 0; phase ^= 1u; }
         }
-        if (lane == 0) {
-          if (w.kb > 0) umma_commit(&tfull[acc]);
-          else mbar_arrive(&tfull[acc]);  // empty contraction: nothing was issued
-          issued = issued || w.kb > 0;
+        tc_fence_after();
+        if (elect_one()) {
+          issue(stage, kb, steps);
+          if (two) issue(stage1, kb + 1, kKBlock / kStep);
         }
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        __syncwarp();
+        issued = true;
+        if (kb == 0 && t + units < tiles) next = tile_of<kRaggedK, kTileLanes>(p, bound, first, t + units);
+        kb += two ? 2 : 1;
+        stage = two ? stage1 : stage;
+        phase = two ? phase1 : phase;
+        if (++stage == nstages) { stage = 0; phase ^= 1u; }
       }
-      // no MMA may still read shared memory or TMEM when the CTA tears down
-      if (lane == 0 && issued) {
-        umma_commit(drain);
-        mbar_wait(drain, 0, nullptr, nullptr);
+      if (elect_one()) {
+        if constexpr (kPair) {
+          const uint32_t f = smem_u32(&tfull[acc]);
+          if (w.kb > 0) {
+            umma_commit_pair(f);
+            umma_commit_pair(mapa_shared(f, 1));
+          } else {  // empty contraction: nothing was issued
+            mbar_arrive_cluster(mapa_shared(f, 0));
+            mbar_arrive_cluster(mapa_shared(f, 1));
+          }
+        } else {
+          if (w.kb > 0) umma_commit(&tfull[acc]);
+          else mbar_arrive(&tfull[acc]);
+        }
+      }
+      __syncwarp();
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    // no MMA may still read shared memory or TMEM when the CTAs tear down
+    if (issued && elect_one()) {
+      if constexpr (kPair) umma_commit_pair(smem_u32(drain));
+      else umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ odd CTA of a pair
+    // dW: clears its part of the blocks that run past their group's end and
+    // tells the issuer.
+    if constexpr (kRaggedK) {
+      uint32_t tail_phases = 0;
+      int blocks = 0;   // k-blocks of the tiles before
+      for (int t = unit; t < tiles; t += units) {
+        const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+        blocks += w.kb;
+        const int valid = w.kvalid - (w.kb - 1) * kKBlock;
+        if (w.kb == 0 || valid % kStep == 0) continue;
+        const int stage = (blocks - 1) % nstages;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tail[stage], (tail_phases >> stage) & 1u, p.status, abort_flag))) break;
+        tail_phases ^= 1u << stage;
+        uint8_t* s_lane = smem + stage * stage_bytes;
+        clear_rows(s_lane, 2, valid, (valid + kStep - 1) / kStep * kStep, lane);
+        fence_proxy_async_cluster();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail[stage]), 0));
       }
     }
   } else {
@@ -388,15 +589,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = lane; i < p.sw_n; i += 32) p.sw_dst[i] = p.sw_src[i];
     if (blockIdx.x == 0 && ew == 1)
       for (int i = 0; i < p.nfin; ++i) ring_finalize_warp(p.fin[i], lane);
-    const uint32_t slab = smem_u32(s_epi + ew * kSlab);
-    const uint8_t* slab_ptr = s_epi + ew * kSlab;
+    uint8_t* const slabs = s_epi + ew * 2 * kSlab;
     // stmatrix: this lane's 16 bytes of column (8 i + lane % 8), block lane / 8, 64-byte swizzle
-    const uint32_t st_addr = slab + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) * 16);
+    const uint32_t st_off = (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) * 16);
+    int slab = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < tiles && !*abort_flag; t += gridDim.x) {
-      const Tile w = tile_of<kRaggedK>(p, bound, first, t);
-      const int n0 = w.lane0 + qd * 32;       // first output column of this warp
+    auto hand_back = [&](int a) {  // this warp is done with accumulator a
+      if (lane == 0) {
+        if constexpr (kPair) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[a]), 0));
+        else mbar_arrive(&tempty[a]);
+      }
+    };
+    for (int t = unit; t < tiles && !*abort_flag; t += units) {
+      const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+      const int n0 = w.lane0 + rank * kLanes + qd * 32;       // first output column of this warp
       const int steps = (w.cols + 31) / 32;
       // per-lane factors, fetched before the wait for the accumulator: this
       // thread's lanes are n0 + 8 j + lane / 4, j = 0..3
@@ -417,27 +624,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint8_t* const d = static_cast<uint8_t*>(p.d) +
                          (static_cast<int64_t>(w.e) * p.stride_d + static_cast<int64_t>(w.col0) * p.ldd) * (OUT == kFP32 ? 4 : 2);
+      const uint32_t ta = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      uint32_t r[2][16];
+      auto load_step = [&](int st) {   // asynchronous until tmem_ld_wait
+        __syncwarp();
+        tmem_ld_16x256b_x4(ta + st * 32, r[0]);
+        tmem_ld_16x256b_x4(ta + (16u << 16) + st * 32, r[1]);
+      };
+      const bool have_k = w.kb > 0;
       if (half >= steps) {
-        if (lane == 0) mbar_arrive(&tempty[acc]);
+        hand_back(acc);
+      } else if (have_k) {
+        load_step(half);
+      } else {  // empty contraction: the MMA never wrote this accumulator
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0u;
       }
       #pragma unroll 1
       for (int st = half; st < steps; st += 2) {
-        uint32_t r[2][16];
-        if (w.kb > 0) {
-          __syncwarp();
-          const uint32_t ta = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(acc * 256 + st * 32);
-          tmem_ld_16x256b_x4(ta, r[0]);
-          tmem_ld_16x256b_x4(ta + (16u << 16), r[1]);
-          tmem_ld_wait();
-        } else {  // empty contraction: the MMA never wrote this accumulator
-          #pragma unroll
-          for (int i = 0; i < 16; ++i) r[0][i] = r[1][i] = 0u;
-        }
-        if (st + 2 >= steps) {  // this warp's last read of the accumulator
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[acc]);
-        }
+        if (have_k) tmem_ld_wait();
         const int c0 = st * 32;               // first column of this step within the tile
         const int live = min(32, w.cols - c0);
         // r[h][4 i + 2 b + u]: lane 16 h + 8 b + lane / 4, column 8 i + 2 (lane % 4) + u
@@ -464,6 +669,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 v[h][4 * i + q] = __uint_as_float(x) * f[0];
             }
         }
+        uint32_t o[16];   // the block's packed pairs, in stmatrix order
+        if constexpr (OUT != kFP32) {
+          #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j)
+              o[4 * i + j] = pack2<OUT>(v[j >> 1][4 * i + 2 * (j & 1)], v[j >> 1][4 * i + 2 * (j & 1) + 1]);
+        }
+        if (st + 2 >= steps) {  // this warp's last read of the accumulator
+          tc_fence_before();
+          __syncwarp();
+          hand_back(acc);
+        } else if (have_k) {    // the next step's values arrive while this one is stored
+          load_step(st + 2);
+        }
         if constexpr (OUT == kFP32) {
           // eight lanes hold 8 consecutive floats of a row: 32-byte sectors, no staging
           float* df = reinterpret_cast<float*>(d);
@@ -476,85 +696,142 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c < live && n < p.nlane) df[static_cast<int64_t>(c0 + c) * p.ldd + n] = v[h][i];
             }
         } else {
+          uint8_t* const buf = slabs + slab * kSlab;
+          if (lane == 0) bulk_wait_read<1>();  // the copy that last read this slab is done
+          __syncwarp();
+          const uint32_t st_addr = smem_u32(buf) + st_off;
           #pragma unroll
           for (int i = 0; i < 4; ++i)
-            stmatrix_x4_trans(st_addr + i * 8 * 64, pack2<OUT>(v[0][4 * i], v[0][4 * i + 1]),
-                              pack2<OUT>(v[0][4 * i + 2], v[0][4 * i + 3]), pack2<OUT>(v[1][4 * i], v[1][4 * i + 1]),
-                              pack2<OUT>(v[1][4 * i + 2], v[1][4 * i + 3]));
-          __syncwarp();
+            stmatrix_x4_trans(st_addr + i * 8 * 64, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           unsigned short* dh = reinterpret_cast<unsigned short*>(d);
-          if (p.vec_ok) {
-            #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-              const int c = it * 8 + (lane >> 2), q = lane & 3;
-              const int n = n0 + q * 8;
-              const uint4 o = *reinterpret_cast<const uint4*>(slab_ptr + c * 64 + ((q ^ ((c >> 1) & 3)) * 16));
-              if (c < live && n < p.nlane) {
-                unsigned short* dst = dh + static_cast<int64_t>(c0 + c) * p.ldd + n;
-                if (n + 8 <= p.nlane) {
-                  *reinterpret_cast<uint4*>(dst) = o;
-                } else {
-                  const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
-                  #pragma unroll
-                  for (int j = 0; j < 8; ++j)
-                    if (n + j < p.nlane) dst[j] = static_cast<unsigned short>(ow[j >> 1] >> (16 * (j & 1)));
+          if (p.tma_store && (kRaggedK || live == 32)) {
+            // a whole block, or one that ends where D does (the copy clips it)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (n0 < p.nlane) tma_store_3d(&t_d, buf, n0, w.col0 + c0, kRaggedK ? w.e : 0);
+              bulk_commit();
+            }
+          } else {
+            // a block that ends with its group: guarded stores
+            __syncwarp();
+            if (p.vec_ok) {
+              #pragma unroll
+              for (int it = 0; it < 4; ++it) {
+                const int c = it * 8 + (lane >> 2), q = lane & 3;
+                const int n = n0 + q * 8;
+                const uint4 x = *reinterpret_cast<const uint4*>(buf + c * 64 + ((q ^ ((c >> 1) & 3)) * 16));
+                if (c < live && n < p.nlane) {
+                  unsigned short* dst = dh + static_cast<int64_t>(c0 + c) * p.ldd + n;
+                  if (n + 8 <= p.nlane) {
+                    *reinterpret_cast<uint4*>(dst) = x;
+                  } else {
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                    #pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                      if (n + j < p.nlane) dst[j] = static_cast<unsigned short>(xw[j >> 1] >> (16 * (j & 1)));
+                  }
                 }
               }
+            } else if (n0 + lane < p.nlane) {
+              // rows that 16-byte stores cannot address: a lane per output column
+              unsigned short* dst = dh + static_cast<int64_t>(c0) * p.ldd + n0 + lane;
+              for (int c = 0; c < live; ++c)
+                dst[static_cast<int64_t>(c) * p.ldd] = *reinterpret_cast<const unsigned short*>(
+                    buf + c * 64 + (((lane >> 3) ^ ((c >> 1) & 3)) * 16) + (lane & 7) * 2);
             }
-          } else if (n0 + lane < p.nlane) {
-            // rows that 16-byte stores cannot address: a lane per output column
-            unsigned short* dst = dh + static_cast<int64_t>(c0) * p.ldd + n0 + lane;
-            for (int c = 0; c < live; ++c)
-              dst[static_cast<int64_t>(c) * p.ldd] = *reinterpret_cast<const unsigned short*>(
-                  slab_ptr + c * 64 + (((lane >> 3) ^ ((c >> 1) & 3)) * 16) + (lane & 7) * 2);
+            if (lane == 0) bulk_commit();  // an empty group: the count of groups stays one per slab
           }
-          __syncwarp();  // the next step overwrites the slab
+          slab ^= 1;
         }
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
+    // the copies' global writes complete on their own; the CTA only has to
+    // outlive their reads of its shared memory
+    if (lane == 0) bulk_wait_read<0>();
   }
 
   tc_fence_before();
-  cta_sync();
+  if constexpr (kPair) cluster_sync();  // no CTA leaves while the other still signals or reads it
+  else cta_sync();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    if constexpr (kPair) tmem_dealloc_pair(tmem_base, kTmemCols);
+    else tmem_dealloc(tmem_base, kTmemCols);
   }
 }
 
-template <bool kInt8, bool kRaggedK, int OUT>
-cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int grid, int dev, cudaStream_t s) {
-  static bool configured[64] = {};
-  auto kernel = grouped_kernel<kInt8, kRaggedK, OUT>;
-  if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <bool kInt8, bool kRaggedK, bool kPair, int OUT>
+cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_t max_tiles, int dev, int sms,
+                         cudaStream_t s) {
+  static int capacity[64] = {};   // CTAs (pairs) that can be resident at once; 0: not yet configured
+  auto kernel = grouped_kernel<kInt8, kRaggedK, kPair, OUT>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  if (!capacity[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
-    configured[dev] = true;
+    int fit = sms;
+    if (kPair) {
+      cfg.gridDim = dim3(2 * (sms / 2));
+      cfg.dynamicSmemBytes = kSmemMax;
+      cfg.attrs = attr + 1;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      cfg.attrs = attr;
+      cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
+    }
+    if (fit <= 0) return cudaErrorInvalidConfiguration;
+    capacity[dev] = fit;
   }
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, maps[0], maps[1], maps[2], p);
+  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(capacity[dev], max_tiles));
+  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * units : units));
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], p);
+}
+
+template <bool kInt8, bool kRaggedK, int OUT>
+cudaError_t launch_out(const CUtensorMap* maps, const GroupedParams& p, bool pair, int64_t max_tiles, int dev, int sms,
+                       cudaStream_t s) {
+  return pair ? launch_build<kInt8, kRaggedK, true, OUT>(maps, p, max_tiles, dev, sms, s)
+              : launch_build<kInt8, kRaggedK, false, OUT>(maps, p, max_tiles, dev, sms, s);
 }
 
 }  // namespace
 
-int grouped_stages(int col_tile) {
-  return std::min(kMaxStages, kOperandBytes / (kLaneBytes + std::max(col_tile, 32) * kKBlock));
+void grouped_smem(GroupedParams* p, bool pair) {
+  const int cols = std::max(pair ? p->col_tile / 2 : p->col_tile, 32);
+  const int stage = kLaneBytes + cols * kKBlock;
+  const int fixed = kFixedSmem + 2 * (p->groups + 1) * 4;
+  p->stages = std::min({kMaxStages, kOperandBytes / stage, (kSmemMax - fixed) / stage});
+  p->smem_bytes = fixed + p->stages * stage;
 }
 
-cudaError_t launch_grouped(const CUtensorMap* maps, const GroupedParams& p, bool int8, bool ragged_k, int out_dtype,
-                           int64_t max_tiles, cudaStream_t s) {
+cudaError_t launch_grouped(const CUtensorMap* maps, const GroupedParams& p, bool int8, bool ragged_k, bool pair,
+                           int out_dtype, int64_t max_tiles, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int sms = num_sms(dev);
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, max_tiles)));
-  if (!int8) return ragged_k ? launch_build<false, true, kBF16>(maps, p, grid, dev, s)
-                             : launch_build<false, false, kBF16>(maps, p, grid, dev, s);
-  if (out_dtype == kFP32) return launch_build<true, false, kFP32>(maps, p, grid, dev, s);
-  if (out_dtype == kFP16) return launch_build<true, false, kFP16>(maps, p, grid, dev, s);
-  return launch_build<true, false, kBF16>(maps, p, grid, dev, s);
+  if (sms <= 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!int8) return ragged_k ? launch_out<false, true, kBF16>(maps, p, pair, max_tiles, dev, sms, s)
+                             : launch_out<false, false, kBF16>(maps, p, pair, max_tiles, dev, sms, s);
+  if (out_dtype == kFP32) return launch_out<true, false, kFP32>(maps, p, pair, max_tiles, dev, sms, s);
+  if (out_dtype == kFP16) return launch_out<true, false, kFP16>(maps, p, pair, max_tiles, dev, sms, s);
+  return launch_out<true, false, kBF16>(maps, p, pair, max_tiles, dev, sms, s);
 }
 
 }  // namespace fp8lin

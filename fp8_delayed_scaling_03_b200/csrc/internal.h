@@ -174,7 +174,7 @@ struct GroupedParams {
   int tiles_lane, tiles_col;  // tiles_col: ragged contraction only
   int k_blocks;               // 128-byte blocks of the contraction (ragged contraction: of all rows)
   int col_tile;               // columns per tile: 16, 32, 64, 128 or 256
-  int stages;
+  int stages, smem_bytes;
   int lane_mn;                // the lane operand is MN-major
   int lane_shared;            // every group uses the same lane operand: batch coordinate 0
   uint32_t idesc;             // without N, which follows each tile's columns
@@ -186,6 +186,7 @@ struct GroupedParams {
   void* d;
   int64_t ldd, stride_d;      // elements; stride_d between groups (ragged contraction)
   int vec_ok;                 // 16-byte stores can address D's rows
+  int tma_store;              // TMA can store whole 32 x 32 blocks of D
   int* status;
   SideWrites side;
   RingFinalize fin[2];
@@ -243,13 +244,17 @@ int gemm_split_factor(int tiles, int k_blocks, int sms, bool forced);
 int gemm_pair_capacity(int device);
 // maps[0..2]: A, B, D of pr[0]; maps[3..5]: those of pr[1] (zeroed if unused).
 cudaError_t launch_gemm(const CUtensorMap* maps, const GemmParams& p, int cfg, cudaStream_t s);
-// Stages of the operand ring for a column tile.
-int grouped_stages(int col_tile);
-// maps: lane operand, column operand (box of col_tile rows), column operand
-// (box of 32 rows; unused by a ragged contraction).  max_tiles: an upper bound
-// on the launch's tiles.  out_dtype: kBF16, or for int8 also kFP16 / kFP32.
-cudaError_t launch_grouped(const CUtensorMap* maps, const GroupedParams& p, bool int8, bool ragged_k, int out_dtype,
-                           int64_t max_tiles, cudaStream_t s);
+// Sets the stages of the operand ring and the shared memory of a launch from
+// its column tile and group count.
+void grouped_smem(GroupedParams* p, bool pair);
+// maps: lane operand, column operand (box of the rows a CTA loads of a whole
+// tile), column operand (box of 32 rows; unused by a ragged contraction), D
+// (32 x 32 blocks; used with tma_store).
+// pair: tiles of 256 lanes on clusters of two CTAs, else 128 on one.
+// max_tiles: an upper bound on the launch's tiles.  out_dtype: kBF16, or for
+// int8 also kFP16 / kFP32.
+cudaError_t launch_grouped(const CUtensorMap* maps, const GroupedParams& p, bool int8, bool ragged_k, bool pair,
+                           int out_dtype, int64_t max_tiles, cudaStream_t s);
 cudaError_t launch_quantize_int8(int in_dtype, const Int8QuantizeParams& p, cudaStream_t s);
 cudaError_t launch_dbias(const DbiasParams& p, cudaStream_t s);
 cudaError_t launch_fill(const FillParams& p, cudaStream_t s);

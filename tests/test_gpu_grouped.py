@@ -107,10 +107,38 @@ def test_weight_gradient(counts, n, k, fmt_g):
         at += m
 
 
-def test_neighbours_nans_stay_out():
+@pytest.mark.parametrize("c,n,k", [([300, 0, 129, 515, 256], 4112, 144), ([257] * 9, 2049, 100), ([1000, 40, 160], 5000, 520),
+                                   ([700, 333, 1, 0, 130], 4096, 1)])
+def test_large_products(c, n, k):
+    """Groups and widths that fill the GPU: tiles on pairs of SMs, forward, dX and dW."""
+    rows, groups = sum(c), len(c)
+    off = offsets_of(c)
+    x8, w8, g8 = codes(rows, k, 0, 1), codes(n, k, 0, 2, batch=groups), codes(rows, n, 1, 3)
+    sx, sw, sg = scales(1, 4), scales(groups, 5), scales(1, 6)
+    y = F.grouped_mm(x8, w8, off, sx, sw)
+    b = F.grouped_linear_backward(g8, F.ForwardResult(None, x8, w8, sx, sw, None, None), off, None, g_scale_in=sg)
+    # dX with the operands' roles exchanged, so that its width is the large one too
+    t8 = w8.transpose(1, 2).contiguous()
+    tp = torch.zeros(groups, k, (n + 15) // 16 * 16, dtype=torch.uint8, device="cuda")
+    tp[:, :, :n] = t8
+    wide = F.grouped_mm(x8, tp[:, :, :n], off, sx, sw, w_major=F.FP8_MN_MAJOR)
+    at = 0
+    for e, m in enumerate(c):
+        x, w, g = value(x8[at:at + m], 0), value(w8[e], 0), value(g8[at:at + m], 1)
+        s, sd, sdw = float(sx) * float(sw[e]), float(sg) * float(sw[e]), float(sg) * float(sx)
+        assert_close(y[at:at + m], x @ w.t() / s, x.abs() @ w.abs().t() / s, ("y", e))
+        assert torch.equal(wide[at:at + m], y[at:at + m])
+        assert_close(b.dx[at:at + m], g @ w / sd, g.abs() @ w.abs() / sd, ("dx", e))
+        assert_close(b.dw[e], g.t() @ x / sdw, g.abs().t() @ x.abs() / sdw, ("dw", e))
+        at += m
+    assert F.fp8_get_device_status() == 0
+
+
+@pytest.mark.parametrize("small", [True, False])
+def test_neighbours_nans_stay_out(small):
     """NaN codes in one group change that group's results alone, though its rows share tiles and k-blocks with others'."""
     c = [5, 33, 70, 129]
-    rows, n, k = sum(c), 144, 96
+    rows, n, k = sum(c), 144 if small else 5120, 96
     off = offsets_of(c)
     x8, g8, w8 = codes(rows, k, 0, 1), codes(rows, n, 1, 2), codes(n, k, 0, 3, batch=len(c))
     sx, sw, sg = scales(1, 4), scales(1, 5), scales(1, 6)

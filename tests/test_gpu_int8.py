@@ -62,6 +62,18 @@ def test_product(m, n, k):
     assert F.fp8_get_device_status() == 0
 
 
+def test_large_product():
+    """Sizes that fill the GPU: tiles on pairs of SMs, the last of them partial in every direction."""
+    m, n, k = 1061, 5013, 400
+    a, b, sa, sb = int8_codes(m, k, 1), int8_codes(n, k, 2), scales(m, 3), scales(n, 4)
+    s = exact_sum(a, b) * sa.double()[:, None] * sb.double()
+    for dtype in WIDE:
+        y = product(a, b, sa, sb, None, torch.empty(m, n, dtype=dtype, device="cuda"))
+        assert_close(y, s, s, dtype, dtype)
+    one_a, one_b = torch.ones(m, device="cuda"), torch.ones(n, device="cuda")
+    assert torch.equal(product(a, b, one_a, one_b, None, torch.empty(m, n, device="cuda")).double(), exact_sum(a, b))
+
+
 def test_sums_are_exact_integers():
     """Scales of one, fp32 output: whole sums below 2^24 come out exactly, the extreme codes among them."""
     for m, n, k in ((3, 50, 900), (40, 130, 1000)):
