@@ -783,7 +783,7 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   const int64_t tl = (c.nlane + tile_lanes - 1) / tile_lanes;
   GroupedParams p;
   std::memset(&p, 0, sizeof(p));
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   std::memset(maps, 0, sizeof(maps));
   int s;
   if (c.ragged_k) {
@@ -791,6 +791,8 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
     if (c.rows > 0) {
       if ((s = make_fp8_map(&maps[0], c.lane_op, c.nlane, c.rows, c.ld_lane, 128))) return s;
       if ((s = make_fp8_map(&maps[1], c.col_op, c.ncol, c.rows, c.ld_col, 128))) return s;
+      if ((s = make_fp8_map(&maps[2], c.lane_op, c.nlane, c.rows, c.ld_lane, 32))) return s;
+      if ((s = make_fp8_map(&maps[3], c.col_op, c.ncol, c.rows, c.ld_col, 32))) return s;
     }
   } else if (c.k > 0) {
     const uint64_t batch = c.stride_lane ? static_cast<uint64_t>(c.groups) : 1;
@@ -799,7 +801,7 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
     if (s) return s;
     if ((s = make_fp8_map(&maps[1], c.col_op, c.k, c.rows, c.ld_col, static_cast<uint32_t>(pair ? tile / 2 : tile)))) return s;
     // (a tile of at most 32 rows is always one whole copy)
-    if (tile > 32 && (s = make_fp8_map(&maps[2], c.col_op, c.k, c.rows, c.ld_col, 32))) return s;
+    if (tile > 32 && (s = make_fp8_map(&maps[3], c.col_op, c.k, c.rows, c.ld_col, 32))) return s;
   }
   p.groups = static_cast<int>(c.groups);
   p.rows = static_cast<int>(c.rows);
@@ -825,15 +827,15 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   p.ldd = c.ldd;
   p.stride_d = c.ragged_k ? c.stride_d : 0;
   p.vec_ok = aligned(c.d, 16) && (c.ldd * 2) % 16 == 0 && (p.stride_d * 2) % 16 == 0;
-  // whole 2-byte blocks through TMA, as in build_problem; a launch whose tiles
+  // whole 2-byte blocks (32 rows x 64 columns) through TMA, as in build_problem; a launch whose tiles
   // are smaller than a block has none
   p.tma_store = p.vec_ok && c.nlane % 8 == 0 && esize(c.d_dtype) == 2 && tile >= 32;
   if (p.tma_store) {
-    s = c.ragged_k ? make_map(&maps[3], c.d, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.nlane, c.ncol, c.ldd * 2, 32, 32,
-                              CU_TENSOR_MAP_SWIZZLE_64B, static_cast<uint64_t>(c.groups),
+    s = c.ragged_k ? make_map(&maps[4], c.d, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.nlane, c.ncol, c.ldd * 2, 64, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B, static_cast<uint64_t>(c.groups),
                               static_cast<uint64_t>(c.stride_d) * 2)
-                   : make_map(&maps[3], c.d, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.nlane, c.rows, c.ldd * 2, 32, 32,
-                              CU_TENSOR_MAP_SWIZZLE_64B);
+                   : make_map(&maps[4], c.d, CU_TENSOR_MAP_DATA_TYPE_UINT16, c.nlane, c.rows, c.ldd * 2, 64, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
     if (s) return s;
   }
   p.status = status_ptr(dev);

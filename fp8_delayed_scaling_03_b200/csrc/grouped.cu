@@ -26,15 +26,16 @@
 //   * dW contracts over the rows of a group: a k-block may run past the
 //     group's end.  Whole 32-row steps past it are not issued; the rows of
 //     the last step past it are set to zero in both operands' shared memory
-//     (in both, since an fp8 NaN of the next group times zero would be NaN).
+//     (in both, since an fp8 NaN of the next group times zero would be NaN) by
+//     a warp of its own, as the block lands.
 // The stages of the operand ring take what shared memory the group tables (8
 // bytes a group) leave: 192 KB up to 190 groups, a stage less beyond.
 // Roles as in gemm.cu: warp 0 lane 0 TMA producer, warp 1 MMA issuer, warps
 // 2-9 epilogue over double-buffered TMEM accumulators, every wait bounded.
 // The epilogue reads 16 lanes x 32 columns per tcgen05.ld.16x256b, whose
 // register layout is the one stmatrix takes: stmatrix.trans turns the block
-// over so that a token's 32 outputs are 64 contiguous bytes in a swizzled slab,
-// which leaves by a TMA store.  A block cut by its group's end (which TMA
+// over so that a token's outputs are contiguous in a swizzled slab (64 lanes =
+// 128 bytes, two warps), which leaves by a TMA store.  A block cut by its group's end (which TMA
 // cannot clip: the next group's rows follow) leaves as 16-byte stores guarded
 // by that end, and one of rows that TMA cannot address as single elements.
 #include <algorithm>
@@ -50,10 +51,12 @@ namespace {
 constexpr int kLanes = 128;              // M side of a tile
 constexpr int kKBlock = 128;             // bytes of the contraction per stage
 constexpr int kStep = 32;                // contraction per MMA
-constexpr int kThreads = 320;            // 10 warps: TMA, MMA, 8 epilogue
 constexpr int kEpiWarps = 8;
-constexpr int kSlab = 32 * 32 * 2;       // one staged 32 x 32 block of 2-byte outputs
-constexpr int kSlabBytes = kEpiWarps * 2 * kSlab;  // two per epilogue warp
+constexpr int kClearWarp = 2 + kEpiWarps; // dW: clears the rows of a group's last block past its end
+constexpr int kThreads = 320;            // 10 warps: TMA, MMA, 8 epilogue
+constexpr int kThreadsRaggedK = kThreads + 32;
+constexpr int kSlab = 32 * 64 * 2;       // one staged block of 2-byte outputs: 32 columns x 64 lanes, two warps
+constexpr int kSlabBytes = kEpiWarps / 2 * 2 * kSlab;  // two per two epilogue warps
 constexpr int kLaneBytes = kLanes * kKBlock;
 constexpr int kOperandBytes = 192 * 1024;
 constexpr int kMaxStages = 10;
@@ -63,7 +66,7 @@ constexpr int kRaster = 8;               // token tiles per raster group
 // Shared memory: [operand stages][slabs][barriers][group bounds, first tiles].
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kFixedSmem = 1024 + kSlabBytes + kBarBytes;
-static_assert((3 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barrier block");
+static_assert((4 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barrier block");
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -94,6 +97,49 @@ __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
+// mbar_wait (device.cuh) whose probes let the hardware suspend the warp for up
+// to a millisecond until the phase completes.  Without the hint a waiting warp
+// probes again and again; eight epilogue warps doing so through a mainloop
+// cost issue slots and, at the power limit, clock.
+template <bool kCluster = false>
+__device__ __forceinline__ bool mbar_await(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  const uint32_t a = smem_u32(bar);
+  auto probe = [&]() {
+    uint32_t ok;
+    if constexpr (kCluster)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(a), "r"(parity), "r"(1000000u)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(a), "r"(parity), "r"(1000000u)
+          : "memory");
+    return ok != 0;
+  };
+  if (probe()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  #pragma unroll 1
+  while (true) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (probe()) return true;
+    if (abort && *abort) return false;
+    if (globaltimer_ns() - t0 > FP8LIN_WAIT_LIMIT_NS) {
+      if (status) atomicExch(status, kDevTimeout);
+      if (abort) *abort = 1;
+      return false;
+    }
+  }
+}
+
 // Whether a phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -105,6 +151,21 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
+}
+
+// Barriers of two epilogue warps (64 threads), the second with a vote.
+__device__ __forceinline__ void duo_sync(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool duo_all(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return r != 0;
 }
 
 // One lane of a converged warp, always the same.
@@ -276,10 +337,10 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int chunks, int from,
 // loads 128 lanes and half of the columns into its own shared memory, the even
 // one issues, and each holds its 128 lanes' accumulators.
 template <bool kInt8, bool kRaggedK, bool kPair, int OUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap t_lane, const __grid_constant__ CUtensorMap t_col,
-                   const __grid_constant__ CUtensorMap t_col32, const __grid_constant__ CUtensorMap t_d,
-                   const __grid_constant__ GroupedParams p) {
+                   const __grid_constant__ CUtensorMap t_lane32, const __grid_constant__ CUtensorMap t_col32,
+                   const __grid_constant__ CUtensorMap t_d, const __grid_constant__ GroupedParams p) {
   constexpr int kTileLanes = kPair ? 2 * kLanes : kLanes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -292,10 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  // pair, dW, one per stage: in the odd CTA its part of a group's last block
-  // landed (bytes); in the even CTA the odd one's part is cleared
-  uint64_t* tail = drain + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + kMaxStages);
+  // dW, one each per stage, for a group's last block that runs past its end:
+  // its bytes landed in this CTA; every CTA's part is cleared (the issuer's CTA)
+  uint64_t* landed = drain + 1;
+  uint64_t* cleared = landed + kMaxStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + kMaxStages);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* bound = reinterpret_cast<int*>(s_epi + kSlabBytes + kBarBytes);
   int* first = bound + p.groups + 1;
@@ -311,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < nstages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      if (kRaggedK && kPair) mbar_init(&tail[s], 1);
+      if (kRaggedK) {
+        mbar_init(&landed[s], 1);
+        mbar_init(&cleared[s], kPair ? 2 : 1);
+      }
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
@@ -324,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.k_blocks > 0) {  // an empty contraction has no maps
       prefetch_tmap(&t_lane);
       prefetch_tmap(&t_col);
-      if (!kRaggedK && p.col_tile > 32) prefetch_tmap(&t_col32);
+      if (kRaggedK) prefetch_tmap(&t_lane32);
+      if (kRaggedK || p.col_tile > 32) prefetch_tmap(&t_col32);
     }
   }
   if (warp == 1) {
@@ -368,18 +434,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* s_col = s_lane + kLaneBytes;
         const int k = w.k0 + kb * kKBlock;
         const int lane_x = p.lane_mn ? lane0 : k, lane_y = p.lane_mn ? k : lane0;
-        if constexpr (kPair) {
-          // Both CTAs' bytes are counted on the even CTA's full barrier -- but
-          // for a block whose last rows have to be cleared: there the odd CTA's
-          // bytes go to its own tail barrier, for the warp that clears.
-          const bool clear = kRaggedK && kb == w.kb - 1 && w.kvalid % kStep != 0;
-          uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
-          if (rank == 0) {
-            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(clear ? bytes : 2 * bytes));
-          } else if (clear) {
-            bar = mapa_shared(smem_u32(&tail[st]), 1);
-            mbar_arrive_expect_tx(&tail[st], static_cast<uint32_t>(bytes));
+        if constexpr (kRaggedK) {
+          const int valid = w.kvalid - kb * kKBlock;
+          if (valid < kKBlock && valid % kStep != 0) {
+            // The group's last block, to be cleared past its end: only the
+            // 32-row steps that hold rows of the group, into this CTA's own
+            // `landed` barrier; `full` just takes its turn.
+            const int parts = (valid + kStep - 1) / kStep;
+            if (rank == 0) mbar_arrive(&full[st]);
+            mbar_arrive_expect_tx(&landed[st], static_cast<uint32_t>(parts * kStep * 128 * (1 + boxes)));
+            for (int i = 0; i < parts; ++i) {
+              tma_load_3d(s_lane + i * kStep * 128, &t_lane32, &landed[st], lane0, k + i * kStep, 0);
+              for (int b = 0; b < boxes; ++b)
+                tma_load_3d(s_col + b * 128 * kKBlock + i * kStep * 128, &t_col32, &landed[st], col0 + b * 128,
+                            k + i * kStep, 0);
+            }
+            return;
           }
+        }
+        if constexpr (kPair) {
+          // both CTAs' bytes are counted on the even CTA's full barrier
+          const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(2 * bytes));
           tma_load_3d_pair(s_lane, &t_lane, bar, lane_x, lane_y, z);
           if constexpr (kRaggedK) {
             tma_load_3d_pair(s_col, &t_col, bar, col0, k, 0);
@@ -412,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage1 = wrap ? 0 : stage + 1;
         const uint32_t phase1 = wrap ? phase ^ 1u : phase;
         const bool second = kb + 1 < w.kb && (issued + 1 < nstages || mbar_test(&empty[stage1], phase1 ^ 1u));
-        ok = __all_sync(0xFFFFFFFFu, issued < nstages || mbar_wait(&empty[stage], phase ^ 1u, p.status, abort_flag));
+        ok = __all_sync(0xFFFFFFFFu, issued < nstages || mbar_await(&empty[stage], phase ^ 1u, p.status, abort_flag));
         if (!ok) break;
         const bool two = __all_sync(0xFFFFFFFFu, second);
         if (elect_one()) {
@@ -433,8 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loop, converged, so that descriptors and loop
     // state stay in uniform registers; one elected lane issues.  (With lane 0
     // alone in the loop a k-block of four MMAs took 0.33 us to issue whatever
-    // its columns, about as long as 256 columns take to compute.)  The lanes
-    // also clear the rows past a group's end for dW.
+    // its columns, about as long as 256 columns take to compute.)
     const uint32_t step_k = p.lane_mn ? kStep * 128 >> 4 : kStep >> 4;   // descriptor units per 32 of the contraction
     constexpr uint32_t kColStep = kRaggedK ? kStep * 128 >> 4 : kStep >> 4;
     const uint32_t smem_base = smem_u32(smem);
@@ -444,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stage_units = static_cast<uint32_t>(stage_bytes) >> 4;
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
-    uint32_t tail_phases = 0;   // one bit per stage
+    uint32_t clear_phases = 0;   // one bit per stage
     bool ok = true, issued = false;
     // the next tile is looked up while the current one's first MMAs run, so
     // that the search is not in the way between two tiles
@@ -458,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = kRaggedK ? (kPair ? 256 : (w.cols + 127) / 128 * 128)
                              : (kPair ? (w.cols + 31) / 32 * 32 : (w.cols + 15) / 16 * 16);
       const uint32_t idesc = p.idesc | static_cast<uint32_t>(n >> 3) << 17;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag));
+      ok = __all_sync(0xFFFFFFFFu, mbar_await(&tempty[acc], acc_phase ^ 1u, p.status, abort_flag));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
@@ -495,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage1 = wrap ? 0 : stage + 1;
         const uint32_t phase1 = wrap ? phase ^ 1u : phase;
         const bool second = kb + 1 < whole && mbar_test(&full[stage1], phase1);
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, p.status, abort_flag));
+        ok = __all_sync(0xFFFFFFFFu, mbar_await(&full[stage], phase, p.status, abort_flag));
         if (!ok) break;
         const bool two = __all_sync(0xFFFFFFFFu, second);
         int steps = kKBlock / kStep;
@@ -504,14 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int valid = w.kvalid - kb * kKBlock;
             steps = (valid + kStep - 1) / kStep;
             if (valid % kStep) {
-              clear_rows(smem + stage * stage_bytes, kPair ? 2 : 1 + (w.cols + 127) / 128, valid, steps * kStep, lane);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if constexpr (kPair) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait<true>(&tail[stage], (tail_phases >> stage) & 1u, p.status, abort_flag));
-                if (!ok) break;
-                tail_phases ^= 1u << stage;
-              }
+              ok = __all_sync(0xFFFFFFFFu,
+                              mbar_await<true>(&cleared[stage], (clear_phases >> stage) & 1u, p.status, abort_flag));
+              if (!ok) break;
+              clear_phases ^= 1u << stage;
             }
           }
         }
@@ -550,31 +621,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (issued && elect_one()) {
       if constexpr (kPair) umma_commit_pair(smem_u32(drain));
       else umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, nullptr);
+      mbar_await(drain, 0, nullptr, nullptr);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ odd CTA of a pair
-    // dW: clears its part of the blocks that run past their group's end and
-    // tells the issuer.
-    if constexpr (kRaggedK) {
-      uint32_t tail_phases = 0;
-      int blocks = 0;   // k-blocks of the tiles before
-      for (int t = unit; t < tiles; t += units) {
-        const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
-        blocks += w.kb;
-        const int valid = w.kvalid - (w.kb - 1) * kKBlock;
-        if (w.kb == 0 || valid % kStep == 0) continue;
-        const int stage = (blocks - 1) % nstages;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tail[stage], (tail_phases >> stage) & 1u, p.status, abort_flag))) break;
-        tail_phases ^= 1u << stage;
-        uint8_t* s_lane = smem + stage * stage_bytes;
-        clear_rows(s_lane, 2, valid, (valid + kStep - 1) / kStep * kStep, lane);
-        fence_proxy_async_cluster();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tail[stage]), 0));
+  } else if (kRaggedK && warp == kClearWarp) {
+    // ------------------------------------------------------------ clearing (dW)
+    // The blocks that run past their group's end, as they land: their rows
+    // past it become zeros in this CTA's operands, while the blocks before
+    // them are multiplied.
+    uint32_t phases = 0;   // one bit per stage
+    int blocks = 0;        // k-blocks up to and with this tile's, less whole turns of the ring
+    for (int t = unit; t < tiles; t += units) {
+      const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+      blocks = (blocks + w.kb) % nstages;
+      const int valid = w.kvalid - (w.kb - 1) * kKBlock;
+      if (w.kb == 0 || valid % kStep == 0) continue;
+      const int stage = blocks == 0 ? nstages - 1 : blocks - 1;
+      if (!__all_sync(0xFFFFFFFFu, mbar_await(&landed[stage], (phases >> stage) & 1u, p.status, abort_flag))) break;
+      phases ^= 1u << stage;
+      clear_rows(smem + stage * stage_bytes, kPair ? 2 : 1 + (w.cols + 127) / 128, valid,
+                 (valid + kStep - 1) / kStep * kStep, lane);
+      fence_proxy_async_cluster();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair) mbar_arrive_cluster(mapa_shared(smem_u32(&cleared[stage]), 0));
+        else mbar_arrive(&cleared[stage]);
       }
     }
-  } else {
+  } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int ew = warp - 2;
     const int qd = warp & 3;          // TMEM lane quadrant of this warp
@@ -589,10 +662,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = lane; i < p.sw_n; i += 32) p.sw_dst[i] = p.sw_src[i];
     if (blockIdx.x == 0 && ew == 1)
       for (int i = 0; i < p.nfin; ++i) ring_finalize_warp(p.fin[i], lane);
-    uint8_t* const slabs = s_epi + ew * 2 * kSlab;
-    // stmatrix: this lane's 16 bytes of column (8 i + lane % 8), block lane / 8, 64-byte swizzle
-    const uint32_t st_off = (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) * 16);
+    // Two warps (64 lanes of the tile) share a slab of [32 columns][128 bytes],
+    // 128-byte swizzle, so that a TMA store writes whole 128-byte lines: with a
+    // warp's 64-byte rows alone the store engine bounded tiles of few k-blocks.
+    const int duo = half * 2 + (qd >> 1);     // which two warps
+    const bool issuer = (qd & 1) == 0;        // of the two: its lane 0 issues the stores
+    uint8_t* const slabs = s_epi + duo * 2 * kSlab;
+    const int chunk0 = (qd & 1) * 4;          // this warp's 16-byte chunks of a row: chunk0 .. chunk0 + 3
+    // stmatrix: this lane's 16 bytes of column (8 i + lane % 8), block lane / 8
+    const uint32_t st_off = (lane & 7) * 128 + (((chunk0 + (lane >> 3)) ^ (lane & 7)) * 16);
     int slab = 0;
+    int held_e = -1;                          // fp8: the group whose factor is held
+    float held_f = 0.0f;
     int acc = 0;
     uint32_t acc_phase = 0;
     auto hand_back = [&](int a) {  // this warp is done with accumulator a
@@ -616,11 +697,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           b[j] = p.bias && n < p.nlane ? load_bias(p.bias, p.bias_dtype, n) : 0.0f;
         }
       } else {
-        f[0] = w.kb > 0 ? 1.0f / (*p.scale_a * p.scale_b[w.e * p.scale_b_step]) : 0.0f;
+        if (w.e != held_e) {
+          held_e = w.e;
+          held_f = 1.0f / (*p.scale_a * p.scale_b[w.e * p.scale_b_step]);
+        }
+        f[0] = w.kb > 0 ? held_f : 0.0f;
       }
-      // a warp leaves together: a lane that gave up must not strand the others
-      // at the next warp barrier
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[acc], acc_phase, p.status, abort_flag))) break;
+      // two warps leave together: a lane that gave up must not strand the
+      // others at the next barrier
+      if (!duo_all(1 + duo, mbar_await(&tfull[acc], acc_phase, p.status, abort_flag))) break;
       tc_fence_after();
       uint8_t* const d = static_cast<uint8_t*>(p.d) +
                          (static_cast<int64_t>(w.e) * p.stride_d + static_cast<int64_t>(w.col0) * p.ldd) * (OUT == kFP32 ? 4 : 2);
@@ -697,30 +782,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
           uint8_t* const buf = slabs + slab * kSlab;
-          if (lane == 0) bulk_wait_read<1>();  // the copy that last read this slab is done
-          __syncwarp();
           const uint32_t st_addr = smem_u32(buf) + st_off;
           #pragma unroll
           for (int i = 0; i < 4; ++i)
-            stmatrix_x4_trans(st_addr + i * 8 * 64, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            stmatrix_x4_trans(st_addr + i * 8 * 128, o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           unsigned short* dh = reinterpret_cast<unsigned short*>(d);
           if (p.tma_store && (kRaggedK || live == 32)) {
-            // a whole block, or one that ends where D does (the copy clips it)
+            // A whole block, or one that ends where D does (the copy clips it).
+            // Past the barrier the other slab is free too: the store that read
+            // it was waited for first.
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
+            if (issuer && lane == 0) bulk_wait_read<0>();
+            duo_sync(1 + duo);
+            if (issuer && lane == 0) {
               if (n0 < p.nlane) tma_store_3d(&t_d, buf, n0, w.col0 + c0, kRaggedK ? w.e : 0);
               bulk_commit();
             }
           } else {
-            // a block that ends with its group: guarded stores
-            __syncwarp();
+            // a block that ends with its group: guarded stores of this warp's part
+            if (issuer && lane == 0) bulk_wait_read<0>();
+            duo_sync(1 + duo);
             if (p.vec_ok) {
               #pragma unroll
               for (int it = 0; it < 4; ++it) {
                 const int c = it * 8 + (lane >> 2), q = lane & 3;
                 const int n = n0 + q * 8;
-                const uint4 x = *reinterpret_cast<const uint4*>(buf + c * 64 + ((q ^ ((c >> 1) & 3)) * 16));
+                const uint4 x = *reinterpret_cast<const uint4*>(buf + c * 128 + (((chunk0 + q) ^ (c & 7)) * 16));
                 if (c < live && n < p.nlane) {
                   unsigned short* dst = dh + static_cast<int64_t>(c0 + c) * p.ldd + n;
                   if (n + 8 <= p.nlane) {
@@ -738,9 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               unsigned short* dst = dh + static_cast<int64_t>(c0) * p.ldd + n0 + lane;
               for (int c = 0; c < live; ++c)
                 dst[static_cast<int64_t>(c) * p.ldd] = *reinterpret_cast<const unsigned short*>(
-                    buf + c * 64 + (((lane >> 3) ^ ((c >> 1) & 3)) * 16) + (lane & 7) * 2);
+                    buf + c * 128 + (((chunk0 + (lane >> 3)) ^ (c & 7)) * 16) + (lane & 7) * 2);
             }
-            if (lane == 0) bulk_commit();  // an empty group: the count of groups stays one per slab
+            __syncwarp();
           }
           slab ^= 1;
         }
@@ -769,7 +856,7 @@ cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_
   static int capacity[64] = {};   // CTAs (pairs) that can be resident at once; 0: not yet configured
   auto kernel = grouped_kernel<kInt8, kRaggedK, kPair, OUT>;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kRaggedK ? kThreadsRaggedK : kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -800,7 +887,7 @@ cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_
   const int64_t units = std::max<int64_t>(1, std::min<int64_t>(capacity[dev], max_tiles));
   cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * units : units));
   cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p);
 }
 
 template <bool kInt8, bool kRaggedK, int OUT>

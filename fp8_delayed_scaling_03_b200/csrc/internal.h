@@ -186,7 +186,7 @@ struct GroupedParams {
   void* d;
   int64_t ldd, stride_d;      // elements; stride_d between groups (ragged contraction)
   int vec_ok;                 // 16-byte stores can address D's rows
-  int tma_store;              // TMA can store whole 32 x 32 blocks of D
+  int tma_store;              // TMA can store whole blocks of D (32 rows x 64 columns)
   int* status;
   SideWrites side;
   RingFinalize fin[2];
@@ -248,8 +248,9 @@ cudaError_t launch_gemm(const CUtensorMap* maps, const GemmParams& p, int cfg, c
 // its column tile and group count.
 void grouped_smem(GroupedParams* p, bool pair);
 // maps: lane operand, column operand (box of the rows a CTA loads of a whole
-// tile), column operand (box of 32 rows; unused by a ragged contraction), D
-// (32 x 32 blocks; used with tma_store).
+// tile), both again with boxes of 32 rows (the lane operand's for a ragged
+// contraction only), D
+// (blocks of 32 rows x 64 columns; used with tma_store).
 // pair: tiles of 256 lanes on clusters of two CTAs, else 128 on one.
 // max_tiles: an upper bound on the launch's tiles.  out_dtype: kBF16, or for
 // int8 also kFP16 / kFP32.
