@@ -66,7 +66,7 @@ constexpr int kRaster = 8;               // token tiles per raster group
 // Shared memory: [operand stages][slabs][barriers][group bounds, first tiles].
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kFixedSmem = 1024 + kSlabBytes + kBarBytes;
-static_assert((4 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barrier block");
+static_assert((4 * kMaxStages + 6) * 8 + 8 <= kBarBytes, "barrier block");
 
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -195,6 +195,21 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
 // group ends inside a k-block, 415 us against 366 for 8192 rows in 8 uneven groups of 11008 x 4096.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 16 bytes into the shared memory of a CTA of the cluster; their arrival is
+// counted on its mbarrier.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+      : "memory");
+}
+
+// Accumulators as register bits: int32 (exact) or fp32 sums.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t add_sums(uint32_t a, uint32_t b) {
+  return kInt8 ? a + b : __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
 
 template <int OUT>
@@ -330,11 +345,14 @@ __device__ __forceinline__ void clear_rows(uint8_t* stage, int chunks, int from,
 // kPair: a cluster of two CTAs runs tiles of 256 lanes with 2-SM MMAs: each CTA
 // loads 128 lanes and half of the columns into its own shared memory, the even
 // one issues, and each holds its 128 lanes' accumulators.
-template <bool kInt8, bool kRaggedK, bool kPair, int OUT>
+// kSplit: a cluster of p.split CTAs shares one tile per launch, each with a
+// share of its k-blocks (few tiles, see pick_grouped_tile).
+template <bool kInt8, bool kRaggedK, bool kPair, bool kSplit, int OUT>
 __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap t_lane, const __grid_constant__ CUtensorMap t_col,
                    const __grid_constant__ CUtensorMap t_lane32, const __grid_constant__ CUtensorMap t_col32,
                    const __grid_constant__ CUtensorMap t_d, const __grid_constant__ GroupedParams p) {
+  static_assert(!kSplit || (!kPair && !kRaggedK), "split tiles are single-CTA tiles of tokens");
   constexpr int kTileLanes = kPair ? 2 * kLanes : kLanes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -351,17 +369,23 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
   // its bytes landed in this CTA; every CTA's part is cleared (the issuer's CTA)
   uint64_t* landed = drain + 1;
   uint64_t* cleared = landed + kMaxStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + kMaxStages);
+  uint64_t* joined = cleared + kMaxStages;  // split tiles, rank 0: the other ranks' partial sums landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* bound = reinterpret_cast<int*>(s_epi + kSlabBytes + kBarBytes);
   int* first = bound + p.groups + 1;
+  // split tiles, rank 0: partial sums of ranks 1 .. split - 1 (16-byte aligned), each [32-column
+  // step][epilogue warp][4 registers][lane] in the epilogue's register order
+  uint8_t* partials = s_epi + kSlabBytes + kBarBytes + (2 * (p.groups + 1) * 4 + 15) / 16 * 16;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nstages = p.stages;
-  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;
-  const int unit = kPair ? static_cast<int>(blockIdx.x) >> 1 : static_cast<int>(blockIdx.x);
-  const int units = kPair ? static_cast<int>(gridDim.x) >> 1 : static_cast<int>(gridDim.x);
+  const int rank = kPair ? static_cast<int>(cluster_rank()) : 0;      // place in the tile's geometry
+  const int part = kSplit ? static_cast<int>(cluster_rank()) : 0;     // share of its k-blocks
+  const int per_unit = kPair ? 2 : (kSplit ? p.split : 1);
+  const int unit = static_cast<int>(blockIdx.x) / per_unit;
+  const int units = static_cast<int>(gridDim.x) / per_unit;
 
   if (threadIdx.x == 64) {
     for (int s = 0; s < nstages; ++s) {
@@ -377,6 +401,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
       mbar_init(&tempty[a], kPair ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(drain, 1);
+    if (kSplit) mbar_init(joined, 1);
     *abort_flag = 0;
     fence_mbar_init();
     if (p.tma_store) prefetch_tmap(&t_d);
@@ -400,12 +425,22 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
   pdl_wait();
   if (warp == 3) scan_groups<kRaggedK>(p, bound, first, lane);
   tc_fence_before();
-  if constexpr (kPair) cluster_sync();  // both CTAs' barriers exist before either signals the other
+  if constexpr (kPair || kSplit) cluster_sync();  // every CTA's barriers exist before another signals them
   else cta_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int tiles = first[p.groups];
   pdl_trigger();
+  // the tile of index t; of a split tile, this CTA's share of the k-blocks
+  auto tile_at = [&](int t) {
+    Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+    if constexpr (kSplit) {
+      const int from = part * w.kb / p.split;
+      w.kb = (part + 1) * w.kb / p.split - from;
+      w.k0 = from * kKBlock;
+    }
+    return w;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -413,7 +448,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     for (int t = unit; t < tiles; t += units) {
-      const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+      const Tile w = tile_at(t);
       // columns this CTA loads: its whole share of the tile in one copy, or
       // as many 32-row copies as hold its share of the remaining tokens
       const int share = kPair ? (w.cols + 31) / 32 * 16 : w.cols;
@@ -518,10 +553,10 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     // the next tile is looked up while the current one's first MMAs run, so
     // that the search is not in the way between two tiles
     Tile w{}, next{};
-    if (unit < tiles) next = tile_of<kRaggedK, kTileLanes>(p, bound, first, unit);
+    if (unit < tiles) next = tile_at(unit);
     for (int t = unit; t < tiles && ok; t += units) {
       w = next;
-      if (w.kb == 0 && t + units < tiles) next = tile_of<kRaggedK, kTileLanes>(p, bound, first, t + units);
+      if (w.kb == 0 && t + units < tiles) next = tile_at(t + units);
       // N: the tile's columns, rounded up to 16 (a pair's: 32); dW's column
       // operand is MN-major in chunks of 128, which it takes whole
       const int n = kRaggedK ? (kPair ? 256 : (w.cols + 127) / 128 * 128)
@@ -587,7 +622,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         }
         __syncwarp();
         issued = true;
-        if (kb == 0 && t + units < tiles) next = tile_of<kRaggedK, kTileLanes>(p, bound, first, t + units);
+        if (kb == 0 && t + units < tiles) next = tile_at(t + units);
         kb += two ? 2 : 1;
         stage = two ? stage1 : stage;
         phase = two ? phase1 : phase;
@@ -625,7 +660,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     uint32_t phases = 0;   // one bit per stage
     int blocks = 0;        // k-blocks up to and with this tile's, less whole turns of the ring
     for (int t = unit; t < tiles; t += units) {
-      const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+      const Tile w = tile_at(t);
       blocks = (blocks + w.kb) % nstages;
       const int valid = w.kvalid - (w.kb - 1) * kKBlock;
       if (w.kb == 0 || valid % kStep == 0) continue;
@@ -677,7 +712,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
       }
     };
     for (int t = unit; t < tiles && !*abort_flag; t += units) {
-      const Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+      const Tile w = tile_at(t);
       const int n0 = w.lane0 + rank * kLanes + qd * 32;       // first output column of this warp
       const int steps = (w.cols + 31) / 32;
       // per-lane factors, fetched before the wait for the accumulator: this
@@ -687,7 +722,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int n = n0 + 8 * j + (lane >> 2);
-          f[j] = n < p.nlane && w.kb > 0 ? __ldg(p.scale_b + n) : 0.0f;
+          f[j] = n < p.nlane && p.k_blocks > 0 ? __ldg(p.scale_b + n) : 0.0f;
           b[j] = p.bias && n < p.nlane ? load_bias(p.bias, p.bias_dtype, n) : 0.0f;
         }
       } else {
@@ -695,12 +730,19 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
           held_e = w.e;
           held_f = 1.0f / (*p.scale_a * p.scale_b[w.e * p.scale_b_step]);
         }
-        f[0] = w.kb > 0 ? held_f : 0.0f;
+        f[0] = (kRaggedK ? w.kb : p.k_blocks) > 0 ? held_f : 0.0f;
       }
       // two warps leave together: a lane that gave up must not strand the
       // others at the next barrier
       if (!duo_all(1 + duo, mbar_await(&tfull[acc], acc_phase, p.status, abort_flag))) break;
       tc_fence_after();
+      if constexpr (kSplit) {
+        if (part == 0) {
+          if (ew == 0 && lane == 0)
+            mbar_arrive_expect_tx(joined, static_cast<uint32_t>((p.split - 1) * steps * 32 * kLanes * 4));
+          if (!duo_all(1 + duo, mbar_await(joined, 0, p.status, abort_flag))) break;
+        }
+      }
       uint8_t* const d = static_cast<uint8_t*>(p.d) +
                          (static_cast<int64_t>(w.e) * p.stride_d + static_cast<int64_t>(w.col0) * p.ldd) * (OUT == kFP32 ? 4 : 2);
       const uint32_t ta = tmem_base + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(acc * 256);
@@ -722,6 +764,33 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
       #pragma unroll 1
       for (int st = half; st < steps; st += 2) {
         if (have_k) tmem_ld_wait();
+        if constexpr (kSplit) {
+          // the other ranks' sums, from the same registers of their epilogue
+          // threads, are added in rank order: the same result every time
+          const int at = (st * 4 + qd) * 8 * 512 + lane * 16;   // 8 x 16 bytes a thread, 512 bytes a warp
+          if (part != 0) {
+            const uint32_t to = mapa_shared(smem_u32(partials + (part - 1) * max(p.col_tile, 32) * kLanes * 4 + at), 0);
+            const uint32_t bar = mapa_shared(smem_u32(joined), 0);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st_async_v4(to + i * 512, r[i >> 2][4 * (i & 3)], r[i >> 2][4 * (i & 3) + 1], r[i >> 2][4 * (i & 3) + 2],
+                          r[i >> 2][4 * (i & 3) + 3], bar);
+            if (st + 2 < steps && have_k) load_step(st + 2);
+            continue;
+          }
+          for (int q = 1; q < p.split; ++q) {
+            const uint8_t* from = partials + (q - 1) * max(p.col_tile, 32) * kLanes * 4 + at;
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4*>(from + i * 512);
+              uint32_t* v = &r[i >> 2][4 * (i & 3)];
+              v[0] = add_sums<kInt8>(v[0], x.x);
+              v[1] = add_sums<kInt8>(v[1], x.y);
+              v[2] = add_sums<kInt8>(v[2], x.z);
+              v[3] = add_sums<kInt8>(v[3], x.w);
+            }
+          }
+        }
         const int c0 = st * 32;               // first column of this step within the tile
         const int live = min(32, w.cols - c0);
         // r[h][4 i + 2 b + u]: lane 16 h + 8 b + lane / 4, column 8 i + 2 (lane % 4) + u
@@ -733,7 +802,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int c = 8 * i + 2 * (lane & 3) + u;
-              s[u] = c < live && w.kb > 0 ? __ldg(p.scale_a + w.col0 + c0 + c) : 0.0f;
+              s[u] = c < live && p.k_blocks > 0 ? __ldg(p.scale_a + w.col0 + c0 + c) : 0.0f;
             }
           }
           #pragma unroll
@@ -834,7 +903,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
   }
 
   tc_fence_before();
-  if constexpr (kPair) cluster_sync();  // no CTA leaves while the other still signals or reads it
+  if constexpr (kPair || kSplit) cluster_sync();  // no CTA leaves while another still signals or writes it
   else cta_sync();
   if (warp == 1) {
     __syncwarp();
@@ -844,23 +913,22 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
   }
 }
 
-template <bool kInt8, bool kRaggedK, bool kPair, int OUT>
+template <bool kInt8, bool kRaggedK, bool kPair, bool kSplit, int OUT>
 cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_t max_tiles, int dev, int sms,
                          cudaStream_t s) {
   static int capacity[64] = {};   // CTAs (pairs) that can be resident at once; 0: not yet configured
-  auto kernel = grouped_kernel<kInt8, kRaggedK, kPair, OUT>;
+  auto kernel = grouped_kernel<kInt8, kRaggedK, kPair, kSplit, OUT>;
+  const int per_unit = kPair ? 2 : (kSplit ? p.split : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kRaggedK ? kThreadsRaggedK : kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(per_unit);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
   if (!capacity[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
@@ -872,23 +940,25 @@ cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_
       cfg.numAttrs = 1;
       e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
       if (e != cudaSuccess) return e;
-      cfg.attrs = attr;
-      cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
     }
     if (fit <= 0) return cudaErrorInvalidConfiguration;
     capacity[dev] = fit;
   }
-  const int64_t units = std::max<int64_t>(1, std::min<int64_t>(capacity[dev], max_tiles));
-  cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * units : units));
-  cfg.numAttrs = kPair ? 2 : 1;
+  // a split launch has a cluster for every tile there can be: each runs one
+  const int64_t units = kSplit ? max_tiles : std::min<int64_t>(capacity[dev], max_tiles);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, units) * per_unit));
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair || kSplit ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], maps[3], maps[4], p);
 }
 
-template <bool kInt8, bool kRaggedK, int OUT>
-cudaError_t launch_out(const CUtensorMap* maps, const GroupedParams& p, bool pair, int64_t max_tiles, int dev, int sms,
-                       cudaStream_t s) {
-  return pair ? launch_build<kInt8, kRaggedK, true, OUT>(maps, p, max_tiles, dev, sms, s)
-              : launch_build<kInt8, kRaggedK, false, OUT>(maps, p, max_tiles, dev, sms, s);
+template <bool kInt8, int OUT>
+cudaError_t launch_tokens(const CUtensorMap* maps, const GroupedParams& p, bool pair, int64_t max_tiles, int dev,
+                          int sms, cudaStream_t s) {
+  if (pair) return launch_build<kInt8, false, true, false, OUT>(maps, p, max_tiles, dev, sms, s);
+  if (p.split > 1) return launch_build<kInt8, false, false, true, OUT>(maps, p, max_tiles, dev, sms, s);
+  return launch_build<kInt8, false, false, false, OUT>(maps, p, max_tiles, dev, sms, s);
 }
 
 }  // namespace
@@ -896,7 +966,8 @@ cudaError_t launch_out(const CUtensorMap* maps, const GroupedParams& p, bool pai
 void grouped_smem(GroupedParams* p, bool pair) {
   const int cols = std::max(pair ? p->col_tile / 2 : p->col_tile, 32);
   const int stage = kLaneBytes + cols * kKBlock;
-  const int fixed = kFixedSmem + 2 * (p->groups + 1) * 4;
+  int fixed = kFixedSmem + 2 * (p->groups + 1) * 4;
+  if (p->split > 1) fixed += 16 + (p->split - 1) * std::max(p->col_tile, 32) * kLanes * 4;
   p->stages = std::min({kMaxStages, kOperandBytes / stage, (kSmemMax - fixed) / stage});
   p->smem_bytes = fixed + p->stages * stage;
 }
@@ -908,11 +979,13 @@ cudaError_t launch_grouped(const CUtensorMap* maps, const GroupedParams& p, bool
   if (e != cudaSuccess) return e;
   const int sms = num_sms(dev);
   if (sms <= 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!int8) return ragged_k ? launch_out<false, true, kBF16>(maps, p, pair, max_tiles, dev, sms, s)
-                             : launch_out<false, false, kBF16>(maps, p, pair, max_tiles, dev, sms, s);
-  if (out_dtype == kFP32) return launch_out<true, false, kFP32>(maps, p, pair, max_tiles, dev, sms, s);
-  if (out_dtype == kFP16) return launch_out<true, false, kFP16>(maps, p, pair, max_tiles, dev, sms, s);
-  return launch_out<true, false, kBF16>(maps, p, pair, max_tiles, dev, sms, s);
+  if (ragged_k)
+    return pair ? launch_build<false, true, true, false, kBF16>(maps, p, max_tiles, dev, sms, s)
+                : launch_build<false, true, false, false, kBF16>(maps, p, max_tiles, dev, sms, s);
+  if (!int8) return launch_tokens<false, kBF16>(maps, p, pair, max_tiles, dev, sms, s);
+  if (out_dtype == kFP32) return launch_tokens<true, kFP32>(maps, p, pair, max_tiles, dev, sms, s);
+  if (out_dtype == kFP16) return launch_tokens<true, kFP16>(maps, p, pair, max_tiles, dev, sms, s);
+  return launch_tokens<true, kBF16>(maps, p, pair, max_tiles, dev, sms, s);
 }
 
 }  // namespace fp8lin

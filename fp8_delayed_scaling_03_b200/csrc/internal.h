@@ -174,6 +174,7 @@ struct GroupedParams {
   int tiles_lane, tiles_col;  // tiles_col: ragged contraction only
   int k_blocks;               // 128-byte blocks of the contraction (ragged contraction: of all rows)
   int col_tile;               // columns per tile: 16, 32, 64, 128 or 256
+  int split;                  // CTAs of a cluster that share each tile's k-blocks (1: none)
   int stages, smem_bytes;
   int lane_mn;                // the lane operand is MN-major
   int lane_shared;            // every group uses the same lane operand: batch coordinate 0
@@ -245,7 +246,7 @@ int gemm_pair_capacity(int device);
 // maps[0..2]: A, B, D of pr[0]; maps[3..5]: those of pr[1] (zeroed if unused).
 cudaError_t launch_gemm(const CUtensorMap* maps, const GemmParams& p, int cfg, cudaStream_t s);
 // Sets the stages of the operand ring and the shared memory of a launch from
-// its column tile and group count.
+// its column tile, group count and split.
 void grouped_smem(GroupedParams* p, bool pair);
 // maps: lane operand, column operand (box of the rows a CTA loads of a whole
 // tile), both again with boxes of 32 rows (the lane operand's for a ragged

@@ -134,6 +134,29 @@ def test_large_products(c, n, k):
     assert F.fp8_get_device_status() == 0
 
 
+@pytest.mark.parametrize("c", [[1], [1, 0, 2, 0, 0, 1, 0, 3], [40, 0, 20], [64], [33], [0, 0, 5]])
+@pytest.mark.parametrize("n,k", [(130, 1024), (400, 1100), (24, 8192), (1000, 2050)])
+@pytest.mark.parametrize("major", ["K", "MN"])
+def test_few_tiles_and_long_contractions(c, n, k, major):
+    """Launches of a few tiles, whose k-blocks several CTAs share: the same result every time."""
+    rows, groups = sum(c), len(c)
+    x8 = codes(rows, k, 0, 1)
+    w8 = codes(n, k, 0, 2, batch=groups) if major == "K" else codes(k, n, 0, 2, batch=groups)
+    off, sx, sw = offsets_of(c), scales(1, 3), scales(groups, 4)
+    y = F.grouped_mm(x8, w8, off, sx, sw, w_major=F.FP8_K_MAJOR if major == "K" else F.FP8_MN_MAJOR)
+    at = 0
+    for e, m in enumerate(c):
+        x, w = value(x8[at:at + m], 0), value(w8[e], 0)
+        w = w if major == "K" else w.t()
+        s = float(sx) * float(sw[e])
+        assert_close(y[at:at + m], x @ w.t() / s, x.abs() @ w.abs().t() / s, (c, e))
+        at += m
+    for _ in range(3):
+        again = F.grouped_mm(x8, w8, off, sx, sw, w_major=F.FP8_K_MAJOR if major == "K" else F.FP8_MN_MAJOR)
+        assert torch.equal(again, y)
+    assert F.fp8_get_device_status() == 0
+
+
 @pytest.mark.parametrize("small", [True, False])
 def test_neighbours_nans_stay_out(small):
     """NaN codes in one group change that group's results alone, though its rows share tiles and k-blocks with others'."""

@@ -51,7 +51,7 @@ def assert_close(got, want, scaled, dtype, what=""):
 
 
 @pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 33, 64, 100, 129, 256, 300])
-@pytest.mark.parametrize("n,k", [(128, 128), (77, 64), (1000, 40), (16, 1), (129, 513), (640, 2048)])
+@pytest.mark.parametrize("n,k", [(128, 128), (77, 64), (1000, 40), (16, 1), (129, 513), (640, 2048), (4096, 1500)])
 def test_product(m, n, k):
     a, b, sa, sb = int8_codes(m, k, 1), int8_codes(n, k, 2), scales(m, 3), scales(n, 4)
     s = exact_sum(a, b) * sa.double()[:, None] * sb.double()
