@@ -724,7 +724,8 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
                             fmt_w=FP8_E4M3, need_dx=True, need_dw=True, g_scale_in=None, dx=None, dw=None,
                             g8=None) -> BackwardResult:
     """dx [rows, K] and dw [groups, N, K] through fp8_linear_grouped_backward, reusing the forward's x8, w8 and scale
-    snapshots.  Rows of dx outside every group are left as they were (or not initialized)."""
+    snapshots.  Rows of dx outside every group are left as they were (or not initialized).  For a g that comes as fp8
+    codes the result's sg is g_scale_in and its amax_g None."""
     groups, off64 = _offsets(offsets)
     M, N, ldg = _matrix(g, "g")
     x8, w8, sx, sw = fwd.x8, fwd.w8, fwd.sx, fwd.sw
@@ -746,16 +747,18 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
         raise ValueError("g8 [rows, N] as uint8 codes")
     dx = _out(dx, (M, K), torch.bfloat16, g, "dx") if need_dx else None
     dw = _out(dw, (groups, N, K), torch.bfloat16, g, "dw") if need_dw else None
-    sc = g.new_empty(2, dtype=torch.float32)
-    at = sc.data_ptr()
+    # a pre-quantized g comes with its scale; one quantized here gets snapshots
+    sc = None if gq else g.new_empty(2, dtype=torch.float32)
+    at = 0 if gq else sc.data_ptr()
     _call("fp8_linear_grouped_backward", dev, _call_grouped_backward,
           _pack_bwd(M, N, K, g.data_ptr(), gd, ldg, _address(g_scale_in), fmt_g, ring_g.H if ring_g is not None else 16,
-                    _address(ring_buf), g8.data_ptr(), _matrix(g8, "g8")[2], at, at + 4,
+                    _address(ring_buf), g8.data_ptr(), _matrix(g8, "g8")[2], at, at and at + 4,
                     x8.data_ptr(), ldx8, sx.data_ptr(), fmt_x, w8.data_ptr(), ldw8, sw.data_ptr(), fmt_w,
                     int(need_dx), int(need_dw), 0, _address(dx), _matrix(dx, "dx")[2] if need_dx else 0,
                     _address(dw), _experts(dw, groups, "dw")[2] if need_dw else 0, 0, 0, 0),
           _pack_groups(groups, offsets.data_ptr(), off64, 0, 0, step))
-    return BackwardResult(dx, dw, None, g8, sc[0:1], sc[1:2])
+    return BackwardResult(dx, dw, None, g8, g_scale_in, None) if gq else \
+        BackwardResult(dx, dw, None, g8, sc[0:1], sc[1:2])
 
 
 def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None):

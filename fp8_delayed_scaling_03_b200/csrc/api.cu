@@ -715,21 +715,6 @@ int validate_quantize(const void* in, int in_dtype, int64_t rows, int64_t cols, 
 
 // ---------------------------------------------------------------- grouped and int8 products
 
-// Column tile of a product whose tokens lie on the MMA's N side: `rows` tokens
-// in `groups` groups, tiles_lane 128-row weight tiles.  The smallest tile that
-// holds one and a half times the average group (a larger group takes several
-// tiles, a smaller one a narrower MMA), halved down to 32 while the launch
-// still fits one wave: more CTAs each stream fewer tokens.
-int pick_col_tile(int64_t rows, int64_t groups, int64_t tiles_lane, int sms) {
-  const int64_t live = std::max<int64_t>(1, std::min(groups, rows));
-  const int64_t want = groups == 1 ? rows : (3 * rows / live + 1) / 2;
-  int t = 16;
-  while (t < 256 && t < want) t *= 2;
-  auto tiles = [&](int64_t c) { return ((rows + live - 1) / live + c - 1) / c * live * tiles_lane; };
-  while (t > 32 && tiles(t / 2) <= sms) t /= 2;
-  return t;
-}
-
 struct GroupedCall {
   int64_t groups = 1;
   const void* offsets = nullptr;
@@ -752,28 +737,52 @@ int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile, int64_t tile_l
   return tl * (c.rows / col_tile + std::min(c.groups, c.rows));
 }
 
-// Tiles of a launch: pairs (256 lanes x 256 columns) where there is enough
-// work to fill the pairs of SMs with them, else one CTA per tile.
-// Few single-CTA tiles leave SMs idle: then clusters of up to 4 CTAs share
-// each tile's k-blocks, at least 4 a CTA (a k-block takes ~0.2 us, joining the
-// sums ~1 us).
+// Tiles of a launch.  A ragged contraction takes CTA pairs (256 x 256) where
+// they fill the pairs of SMs, else 128 x 128 on one CTA.  Products of tokens
+// take the cheapest of
+//   one CTA, 128 lanes x t columns, t = 16 .. 256;
+//   the same with its k-blocks split over a cluster of 2 .. 4 CTAs (few tiles
+//   and a long contraction);
+//   a CTA pair, 256 lanes x 256 columns,
+// by the time of the most loaded CTA: waves x (k-blocks x time of one +
+// epilogue), with the times in microseconds measured on a B200: a k-block of
+// up to 32 columns 0.20, 64 0.24, 128 0.31, 256 columns 0.37 on one CTA as on a
+// pair; an epilogue step (32 columns, two at a time) 0.33; joining split sums
+// 1.0.  Group sizes are not known here: a group is taken to be a quarter
+// larger than the average.  Where the weights' bytes bound the time the
+// choices hardly differ, and the smallest tile, which loads the fewest tokens,
+// comes first.
 void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair, int* split) {
+  const int64_t tl = (c.nlane + 127) / 128, tl2 = (c.nlane + 255) / 256;
   *split = 1;
-  const int64_t tl2 = (c.nlane + 255) / 256;
+  *tile = 256;
   if (c.ragged_k) {
     *pair = tl2 * ((c.ncol + 255) / 256) * c.groups >= sms / 2;
-    *tile = *pair ? 256 : 128;
+    if (!*pair) *tile = 128;
     return;
   }
   const int64_t live = std::max<int64_t>(1, std::min(c.groups, c.rows));
-  const int64_t avg = (c.rows + live - 1) / live;
-  *pair = avg > 128 && (avg + 255) / 256 * live * tl2 >= sms / 2;
-  const int64_t tl = (c.nlane + 127) / 128;
-  *tile = *pair ? 256 : pick_col_tile(c.rows, c.groups, tl, sms);
-  if (!*pair && *tile <= 64) {
-    const int64_t tiles = (avg + *tile - 1) / *tile * live * tl;
-    const int64_t s = std::min<int64_t>({4, sms / std::max<int64_t>(1, tiles), (c.k + 127) / 128 / 4});
-    *split = static_cast<int>(std::max<int64_t>(1, s));
+  const double rows = c.groups == 1 ? static_cast<double>(c.rows)
+                                    : std::max(1.0, 1.25 * static_cast<double>(c.rows) / static_cast<double>(live));
+  const int64_t kb = (c.k + 127) / 128;
+  auto col_tiles = [&](int64_t t) { return static_cast<int64_t>(std::ceil(rows / static_cast<double>(t))) * live; };
+  auto waves = [&](int64_t units, int64_t slots) { return static_cast<double>((units + slots - 1) / slots); };
+  *pair = true;
+  double best = waves(col_tiles(256) * tl2, std::max(1, sms / 2)) * (0.37 * static_cast<double>(kb) + 4 * 0.33);
+  for (int64_t t = 16; t <= 256; t *= 2) {
+    const double t_kb = t <= 32 ? 0.20 : (t == 64 ? 0.24 : (t == 128 ? 0.31 : 0.37));
+    const double epilogue = 0.33 * static_cast<double>((t + 63) / 64);
+    for (int64_t s = 1; s <= 4; ++s) {
+      if (s > 1 && (t > 128 || s * 4 > kb || (s - 1) * t > 192 || col_tiles(t) * tl * s > sms)) break;
+      const double us = waves(col_tiles(t) * tl * s, sms) * (t_kb * static_cast<double>((kb + s - 1) / s) + epilogue) +
+                        (s > 1 ? 1.0 : 0.0);
+      if (us < best * 0.999) {
+        best = us;
+        *pair = false;
+        *tile = static_cast<int>(t);
+        *split = static_cast<int>(s);
+      }
+    }
   }
 }
 
@@ -1550,9 +1559,10 @@ int fp8_linear_grouped_backward(const fp8_linear_bwd_args* a, const fp8_groups* 
   if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP8_ERR_INVALID_ARG;
   if (g->stride_b != 0 || g->stride_d != 0) return FP8_ERR_INVALID_ARG;
   if (!is_fmt(a->fmt_g) || !is_fmt(a->fmt_x) || !is_fmt(a->fmt_w)) return FP8_ERR_INVALID_ARG;
-  if (!a->sg_out || (M > 0 && N > 0 && !a->g)) return FP8_ERR_INVALID_ARG;
+  if (M > 0 && N > 0 && !a->g) return FP8_ERR_INVALID_ARG;
   if (a->need_dbias) return FP8_ERR_UNSUPPORTED;
   const bool gq = is_fp8(a->g_dtype);
+  if (!gq && !a->sg_out) return FP8_ERR_INVALID_ARG;
   if (!gq && !is_wide(a->g_dtype)) return FP8_ERR_INVALID_ARG;
   if (gq) {
     if (a->g_dtype - FP8_DT_E4M3 != a->fmt_g || !a->g_scale_in) return FP8_ERR_INVALID_ARG;
@@ -1597,7 +1607,7 @@ int fp8_linear_grouped_backward(const fp8_linear_bwd_args* a, const fp8_groups* 
   bool side_pending = false;
   if (g_live && gq) {
     side.copy_src[0] = a->g_scale_in; side.copy_dst[0] = a->sg_out; side.zero_dst[0] = a->amax_g_out;
-    side_pending = true;
+    side_pending = a->sg_out || a->amax_g_out;
   } else if (g_live) {
     const bool follows = dx_live || dw_live;
     if (follows && a->ring_g) fin[nfin++] = ring_fin(a->ring_g, a->hist_len, a->fmt_g, a->amax_g_out);

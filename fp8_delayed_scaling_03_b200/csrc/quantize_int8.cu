@@ -13,10 +13,9 @@
 //
 // The cast multiplies by 127 / amax in fp32: two roundings, at most 1.6e-5 off
 // for |t| <= 127.  Only a value that close to the border of two codes can come
-// out wrong, so those (one in some 25,000) are taken again as a 64-bit
-// quotient, whose rounding cannot cross a border: with 24-bit operands the
-// quotient is either exactly on it or at least 2^-33 away.  Codes therefore
-// depend on the values alone, not on how the quotient is computed.
+// out wrong, so for those (one in some 25,000) 254 |x| is compared with
+// (2 k + 1) amax, which 64 bits hold exactly.  Codes therefore depend on the
+// values alone, not on how the quotient is computed.
 #include <type_traits>
 
 #include "device.cuh"
@@ -30,6 +29,8 @@ constexpr int kChunk = 16;     // elements per 16-byte store of codes
 constexpr int kHeld = 2;       // chunks a thread keeps in registers
 constexpr int kMaxThreads = 512;  // 128 registers a thread
 constexpr float kBorder = 0.5f - 2e-5f;
+constexpr float kTinyAmax = 1e-36f;   // 127 / kTinyAmax is below the largest float
+constexpr float kUp = 1.2676506002282294e30f;  // 2^100
 
 template <typename T>
 struct Chunk {
@@ -78,28 +79,37 @@ __device__ __forceinline__ uint32_t chunk_max(const Chunk<T>& c, uint32_t m) {
   return m;
 }
 
-// 16 codes.  border: values whose distance from the nearest integer exceeds it
-// are recomputed in 64 bits (all of them when it is negative).
-template <typename T>
-__device__ __forceinline__ uint4 cast_chunk(const Chunk<T>& c, float inv, float amax, float border) {
+// 16 codes.  kTiny: amax is so small that 127 / amax overflows; values and amax
+// are then taken times 2^100, which is exact.
+template <typename T, bool kTiny>
+__device__ __forceinline__ uint4 cast_chunk(const Chunk<T>& c, float amax) {
   // t + 1.5 * 2^23 rounds t to the nearest integer (ties to even) and holds it
   // in its low bits, two's complement
   constexpr float kMagic = 12582912.0f;
+  const float top = kTiny ? amax * kUp : amax;
+  const float inv = __fdiv_rn(127.0f, top);
+  auto scaled = [&](int j) { return kTiny ? value<T>(c, j) * kUp : value<T>(c, j); };
   uint32_t q[kChunk];
   bool near = false;
   #pragma unroll
   for (int j = 0; j < kChunk; ++j) {
-    const float t = value<T>(c, j) * inv;
+    const float t = __fmul_rn(scaled(j), inv);
     const float m = __fadd_rn(t, kMagic);
     q[j] = __float_as_uint(m);
-    near = near || !(fabsf(__fsub_rn(t, __fsub_rn(m, kMagic))) <= border);
+    near = near || fabsf(__fsub_rn(t, __fsub_rn(m, kMagic))) > kBorder;
   }
   if (near) {
     #pragma unroll
     for (int j = 0; j < kChunk; ++j) {
-      const float t = value<T>(c, j) * inv;
-      if (!(fabsf(t - rintf(t)) <= border))
-        q[j] = static_cast<uint32_t>(__double2int_rn(127.0 * static_cast<double>(value<T>(c, j)) / static_cast<double>(amax)));
+      const float v = scaled(j), t = __fmul_rn(v, inv);
+      if (fabsf(t - rintf(t)) > kBorder) {
+        // |t| is within 1.6e-5 of k + 0.5: which side 127 |v| / top lies on,
+        // from two products that 64 bits hold exactly
+        const int k = static_cast<int>(fabsf(t));
+        const double lhs = 254.0 * static_cast<double>(fabsf(v)), rhs = static_cast<double>(2 * k + 1) * static_cast<double>(top);
+        const int a = lhs > rhs || (lhs == rhs && (k & 1)) ? k + 1 : k;
+        q[j] = static_cast<uint32_t>(v < 0.0f ? -a : a);
+      }
     }
   }
   uint32_t w[4];
@@ -107,6 +117,14 @@ __device__ __forceinline__ uint4 cast_chunk(const Chunk<T>& c, float inv, float 
   for (int i = 0; i < 4; ++i)
     w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040), __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The codes of a chunk of a row whose largest magnitude has the given bits.
+template <typename T>
+__device__ __forceinline__ uint4 codes(const Chunk<T>& c, uint32_t bits) {
+  if (bits == 0u || bits >= 0x7F800000u) return make_uint4(0u, 0u, 0u, 0u);
+  const float amax = __uint_as_float(bits);
+  return amax < kTinyAmax ? cast_chunk<T, true>(c, amax) : cast_chunk<T, false>(c, amax);
 }
 
 // blockDim.y rows a block, blockDim.x threads a row (one warp when there is
@@ -138,28 +156,17 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_int8_kernel(const Int8Qu
     const int lane = threadIdx.x & 31;
     bits = __reduce_max_sync(0xFFFFFFFFu, lane < static_cast<int>(blockDim.x >> 5) ? warp_max[lane] : 0u);
   }
-  const float amax = __uint_as_float(bits);
-  float inv = 0.0f, scale = 1.0f, border = 1.0f, top = 1.0f;
-  if (bits >= 0x7F800000u) {
-    scale = __uint_as_float(0x7FFFFFFFu);
-  } else if (bits) {
-    inv = __fdiv_rn(127.0f, amax);
-    scale = __fdiv_rn(amax, 127.0f);
-    border = isinf(inv) ? -1.0f : kBorder;
-    top = amax;
-  }
-  const bool zero = bits == 0u || bits >= 0x7F800000u;
-  if (live && tid == 0) p.scale[r] = scale;
+  if (live && tid == 0)
+    p.scale[r] = bits >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu)
+                                     : (bits ? __fdiv_rn(__uint_as_float(bits), 127.0f) : 1.0f);
   int8_t* out = p.out + (live ? r : 0) * p.ld_out;
   #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (tid + i * step < chunks)
-      *reinterpret_cast<uint4*>(out + (tid + i * step) * kChunk) =
-          zero ? make_uint4(0u, 0u, 0u, 0u) : cast_chunk<T>(held[i], inv, top, border);
+      *reinterpret_cast<uint4*>(out + (tid + i * step) * kChunk) = codes<T>(held[i], bits);
   for (int64_t c = tid + kHeld * step; c < chunks; c += step)
     *reinterpret_cast<uint4*>(out + c * kChunk) =
-        zero ? make_uint4(0u, 0u, 0u, 0u)
-             : cast_chunk<T>(load_chunk<T>(row, c * kChunk, p.cols, p.vec_ok), inv, top, border);
+        codes<T>(load_chunk<T>(row, c * kChunk, p.cols, p.vec_ok), bits);
 }
 
 }  // namespace

@@ -476,7 +476,8 @@ FP8LIN_API int fp8_linear_backward(const fp8_linear_bwd_args* args, fp8_stream_t
  * with one ring (scale_b_step 0); a pre-quantized w may come with one scale
  * per group instead (scale_b_step 1): then w_scale_in, sw_out and the
  * backward's sw hold `groups` values.  scale_b_step 1 with a w that is not fp8
- * is FP8_ERR_INVALID_ARG, a bias or need_dbias FP8_ERR_UNSUPPORTED. */
+ * is FP8_ERR_INVALID_ARG, a bias or need_dbias FP8_ERR_UNSUPPORTED.  With a
+ * pre-quantized g, sg_out may be NULL. */
 FP8LIN_API int fp8_linear_grouped_forward(const fp8_linear_fwd_args* args, const fp8_groups* groups,
                                           fp8_stream_t stream);
 FP8LIN_API int fp8_linear_grouped_backward(const fp8_linear_bwd_args* args, const fp8_groups* groups,

@@ -97,8 +97,7 @@ def test_weight_gradient(counts, n, k, fmt_g):
     sg = scales(1, 10)
     b = F.grouped_linear_backward(g8, fwd, off, None, fmt_g=fmt_g, need_dx=False, g_scale_in=sg)
     assert b.dx is None and F.fp8_get_device_status() == 0
-    if rows:  # an empty operand's snapshot is left as it was
-        assert float(b.sg) == float(sg) and float(b.amax_g) == 0.0
+    assert b.sg is sg and b.amax_g is None   # a pre-quantized g's scale is the caller's
     at = front
     for e, m in enumerate(c):
         x, g = value(x8[at:at + m], 0), value(g8[at:at + m], fmt_g)
