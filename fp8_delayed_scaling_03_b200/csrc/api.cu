@@ -789,7 +789,7 @@ void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair, int
 // One launch of a validated call with at least one group and lane.
 int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = nullptr,
                 const RingFinalize* fin = nullptr, int nfin = 0, const float* sw_src = nullptr,
-                float* sw_dst = nullptr, int sw_n = 0) {
+                float* sw_dst = nullptr, int sw_n = 0, bool behind_independent = false) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -863,6 +863,7 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   if (side) p.side = *side;
   for (int i = 0; i < nfin; ++i) p.fin[i] = fin[i];
   p.nfin = nfin;
+  p.late_wait = behind_independent ? 1 : 0;
   p.sw_src = sw_src;
   p.sw_dst = sw_dst;
   p.sw_n = sw_n;
@@ -1621,7 +1622,8 @@ int fp8_linear_grouped_backward(const fp8_linear_bwd_args* a, const fp8_groups* 
     nfin = 0;
   }
   if (dw_live) {
-    if ((s = run_grouped(cw, st, side_pending ? &side : nullptr, fin, nfin))) return s;
+    // (behind dX, which neither reads nor writes what dW does)
+    if ((s = run_grouped(cw, st, side_pending ? &side : nullptr, fin, nfin, nullptr, nullptr, 0, dx_live))) return s;
     side_pending = false;
   }
   if (side_pending) {

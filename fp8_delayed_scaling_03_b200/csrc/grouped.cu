@@ -212,6 +212,17 @@ __device__ __forceinline__ uint32_t add_sums(uint32_t a, uint32_t b) {
   return kInt8 ? a + b : __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
 
+// (a, b) = (x f, y f), one instruction.
+__device__ __forceinline__ void mul_x2(float& a, float& b, float x, float y, float f) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%2, %3};\n\t"
+      "mov.b64 q, {%4, %4};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "f"(x), "f"(y), "f"(f));
+}
+
 template <int OUT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (OUT == kFP16) {
@@ -236,46 +247,83 @@ struct Tile {
   int e, col0, cols, lane0, kb, k0, kvalid;
 };
 
-template <bool kRaggedK, int kTileLanes>
-__device__ __forceinline__ Tile tile_of(const GroupedParams& p, const int* bound, const int* first, int t) {
+// The tile of index t of a product of tokens: the group whose tiles hold t,
+// then groups of kRaster column tiles, lane tile by lane tile.
+template <int kTileLanes>
+__device__ __forceinline__ Tile token_tile(const GroupedParams& p, const int* bound, const int* first, int t) {
   Tile w;
-  if constexpr (kRaggedK) {
-    const int per = p.tiles_lane * p.tiles_col;
-    w.e = t / per;
-    t -= w.e * per;
-    const int tl = t % p.tiles_lane, tc = t / p.tiles_lane;
-    w.lane0 = tl * kTileLanes;
-    w.col0 = tc * p.col_tile;
-    w.cols = min(p.col_tile, p.ncol - w.col0);
-    w.k0 = bound[w.e];
-    w.kvalid = bound[w.e + 1] - w.k0;
-    w.kb = (w.kvalid + kKBlock - 1) / kKBlock;
-  } else {
-    // the group whose tiles hold t: the largest e with first[e] <= t and tiles of its own
-    int lo = 0, hi = p.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    w.e = lo;
-    t -= first[lo];
-    const int row0 = bound[lo], rows = bound[lo + 1] - row0;
-    const int tiles_col = (rows + p.col_tile - 1) / p.col_tile;
-    const int per = kRaster * p.tiles_lane;
-    const int g = t / per;
-    const int gc = min(kRaster, tiles_col - g * kRaster);
-    t -= g * per;
-    const int tc = g * kRaster + t % gc;
-    w.lane0 = (t / gc) * kTileLanes;
-    w.col0 = row0 + tc * p.col_tile;
-    w.cols = min(p.col_tile, row0 + rows - w.col0);
-    w.k0 = 0;
-    w.kvalid = 0;
-    w.kb = p.k_blocks;
+  // the largest e with first[e] <= t and tiles of its own
+  int lo = 0, hi = p.groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid;
   }
+  w.e = lo;
+  t -= first[lo];
+  const int row0 = bound[lo], rows = bound[lo + 1] - row0;
+  const int tiles_col = (rows + p.col_tile - 1) / p.col_tile;
+  const int per = kRaster * p.tiles_lane;
+  const int g = t / per;
+  const int gc = min(kRaster, tiles_col - g * kRaster);
+  t -= g * per;
+  const int tc = g * kRaster + t % gc;
+  w.lane0 = (t / gc) * kTileLanes;
+  w.col0 = row0 + tc * p.col_tile;
+  w.cols = min(p.col_tile, row0 + rows - w.col0);
+  w.k0 = 0;
+  w.kvalid = 0;
+  w.kb = p.k_blocks;
   return w;
 }
+
+// The tiles unit, unit + units, ... of a launch, one after another.  A ragged
+// contraction has the same tiles in every group, so its cursor is a mixed-radix
+// counter (group, column tile, lane tile) that adds the digits of `units`:
+// three divisions once, none per tile, which tiles of one or two k-blocks feel.
+template <bool kRaggedK, int kTileLanes>
+struct Cursor {
+  int t, units;
+  int e, tc, tl, de, dtc, dtl;   // kRaggedK
+  __device__ __forceinline__ Cursor(const GroupedParams& p, int unit, int units_) : t(unit), units(units_) {
+    if constexpr (kRaggedK) {
+      const int per = p.tiles_lane * p.tiles_col;
+      e = unit / per;
+      tc = (unit - e * per) / p.tiles_lane;
+      tl = unit - e * per - tc * p.tiles_lane;
+      de = units / per;
+      dtc = (units - de * per) / p.tiles_lane;
+      dtl = units - de * per - dtc * p.tiles_lane;
+    }
+  }
+  __device__ __forceinline__ void advance(const GroupedParams& p) {
+    t += units;
+    if constexpr (kRaggedK) {
+      tl += dtl;
+      int carry = tl >= p.tiles_lane;
+      tl -= carry ? p.tiles_lane : 0;
+      tc += dtc + carry;
+      carry = tc >= p.tiles_col;
+      tc -= carry ? p.tiles_col : 0;
+      e += de + carry;
+    }
+  }
+  __device__ __forceinline__ Tile tile(const GroupedParams& p, const int* bound, const int* first) const {
+    if constexpr (kRaggedK) {
+      Tile w;
+      w.e = e;
+      w.lane0 = tl * kTileLanes;
+      w.col0 = tc * p.col_tile;
+      w.cols = min(p.col_tile, p.ncol - w.col0);
+      w.k0 = bound[e];
+      w.kvalid = bound[e + 1] - w.k0;
+      w.kb = (w.kvalid + kKBlock - 1) / kKBlock;
+      return w;
+    } else {
+      return token_tile<kTileLanes>(p, bound, first, t);
+    }
+  }
+};
 
 // Group bounds (clamped to the buffer and made non-decreasing by a running
 // maximum, so that no offset can lead outside it or let two groups share a
@@ -293,8 +341,8 @@ __device__ __forceinline__ void scan_groups(const GroupedParams& p, int* bound, 
     return;
   }
   auto offset = [&](int i) {
-    const int64_t v = p.off64 ? static_cast<const int64_t*>(p.offsets)[i]
-                              : static_cast<int64_t>(static_cast<const int*>(p.offsets)[i]);
+    const int64_t v = p.off64 ? static_cast<int64_t>(__ldcg(static_cast<const long long*>(p.offsets) + i))
+                              : static_cast<int64_t>(__ldcg(static_cast<const int*>(p.offsets) + i));
     return static_cast<int>(min(max(v, static_cast<int64_t>(0)), static_cast<int64_t>(p.rows)));
   };
   top = offset(0);
@@ -421,8 +469,10 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
       tmem_relinquish();
     }
   }
-  // Offsets, operands and scales may be the previous kernel's output.
-  pdl_wait();
+  // Offsets, operands and scales may be the previous kernel's output.  A
+  // launch behind an independent product (dW behind dX) waits at its end
+  // instead, see late_wait.
+  if (!p.late_wait) pdl_wait();
   if (warp == 3) scan_groups<kRaggedK>(p, bound, first, lane);
   tc_fence_before();
   if constexpr (kPair || kSplit) cluster_sync();  // every CTA's barriers exist before another signals them
@@ -431,9 +481,10 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int tiles = first[p.groups];
   pdl_trigger();
-  // the tile of index t; of a split tile, this CTA's share of the k-blocks
-  auto tile_at = [&](int t) {
-    Tile w = tile_of<kRaggedK, kTileLanes>(p, bound, first, t);
+  // the tile a role's cursor is at; of a split tile, this CTA's share of the k-blocks
+  using Tiles = Cursor<kRaggedK, kTileLanes>;
+  auto tile_at = [&](const Tiles& at) {
+    Tile w = at.tile(p, bound, first);
     if constexpr (kSplit) {
       const int from = part * w.kb / p.split;
       w.kb = (part + 1) * w.kb / p.split - from;
@@ -447,8 +498,8 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     // (the whole warp, converged, one elected lane issues: see the MMA issuer)
     int stage = 0, issued = 0;
     uint32_t phase = 0;
-    for (int t = unit; t < tiles; t += units) {
-      const Tile w = tile_at(t);
+    for (Tiles at(p, unit, units); at.t < tiles; at.advance(p)) {
+      const Tile w = tile_at(at);
       // columns this CTA loads: its whole share of the tile in one copy, or
       // as many 32-row copies as hold its share of the remaining tokens
       const int share = kPair ? (w.cols + 31) / 32 * 16 : w.cols;
@@ -553,10 +604,12 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     // the next tile is looked up while the current one's first MMAs run, so
     // that the search is not in the way between two tiles
     Tile w{}, next{};
-    if (unit < tiles) next = tile_at(unit);
-    for (int t = unit; t < tiles && ok; t += units) {
+    Tiles at(p, unit, units);
+    if (at.t < tiles) next = tile_at(at);
+    while (at.t < tiles && ok) {
       w = next;
-      if (w.kb == 0 && t + units < tiles) next = tile_at(t + units);
+      at.advance(p);
+      if (w.kb == 0 && at.t < tiles) next = tile_at(at);
       // N: the tile's columns, rounded up to 16 (a pair's: 32); dW's column
       // operand is MN-major in chunks of 128, which it takes whole
       const int n = kRaggedK ? (kPair ? 256 : (w.cols + 127) / 128 * 128)
@@ -622,7 +675,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         }
         __syncwarp();
         issued = true;
-        if (kb == 0 && t + units < tiles) next = tile_at(t + units);
+        if (kb == 0 && at.t < tiles) next = tile_at(at);
         kb += two ? 2 : 1;
         stage = two ? stage1 : stage;
         phase = two ? phase1 : phase;
@@ -659,8 +712,8 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     // them are multiplied.
     uint32_t phases = 0;   // one bit per stage
     int blocks = 0;        // k-blocks up to and with this tile's, less whole turns of the ring
-    for (int t = unit; t < tiles; t += units) {
-      const Tile w = tile_at(t);
+    for (Tiles at(p, unit, units); at.t < tiles; at.advance(p)) {
+      const Tile w = tile_at(at);
       blocks = (blocks + w.kb) % nstages;
       const int valid = w.kvalid - (w.kb - 1) * kKBlock;
       if (w.kb == 0 || valid % kStep == 0) continue;
@@ -711,8 +764,8 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         else mbar_arrive(&tempty[a]);
       }
     };
-    for (int t = unit; t < tiles && !*abort_flag; t += units) {
-      const Tile w = tile_at(t);
+    for (Tiles at(p, unit, units); at.t < tiles && !*abort_flag; at.advance(p)) {
+      const Tile w = tile_at(at);
       const int n0 = w.lane0 + rank * kLanes + qd * 32;       // first output column of this warp
       const int steps = (w.cols + 31) / 32;
       // per-lane factors, fetched before the wait for the accumulator: this
@@ -728,7 +781,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
       } else {
         if (w.e != held_e) {
           held_e = w.e;
-          held_f = 1.0f / (*p.scale_a * p.scale_b[w.e * p.scale_b_step]);
+          held_f = 1.0f / (__ldcg(p.scale_a) * __ldcg(p.scale_b + w.e * p.scale_b_step));
         }
         f[0] = (kRaggedK ? w.kb : p.k_blocks) > 0 ? held_f : 0.0f;
       }
@@ -767,9 +820,9 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         if constexpr (kSplit) {
           // the other ranks' sums, from the same registers of their epilogue
           // threads, are added in rank order: the same result every time
-          const int at = (st * 4 + qd) * 8 * 512 + lane * 16;   // 8 x 16 bytes a thread, 512 bytes a warp
+          const int slot = (st * 4 + qd) * 8 * 512 + lane * 16;   // 8 x 16 bytes a thread, 512 bytes a warp
           if (part != 0) {
-            const uint32_t to = mapa_shared(smem_u32(partials + (part - 1) * max(p.col_tile, 32) * kLanes * 4 + at), 0);
+            const uint32_t to = mapa_shared(smem_u32(partials + (part - 1) * max(p.col_tile, 32) * kLanes * 4 + slot), 0);
             const uint32_t bar = mapa_shared(smem_u32(joined), 0);
             #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -779,7 +832,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
             continue;
           }
           for (int q = 1; q < p.split; ++q) {
-            const uint8_t* from = partials + (q - 1) * max(p.col_tile, 32) * kLanes * 4 + at;
+            const uint8_t* from = partials + (q - 1) * max(p.col_tile, 32) * kLanes * 4 + slot;
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint4 x = *reinterpret_cast<const uint4*>(from + i * 512);
@@ -813,8 +866,8 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
               if constexpr (kInt8)
                 v[h][4 * i + q] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(x)), s[q & 1]), f[2 * h + (q >> 1)]),
                                             b[2 * h + (q >> 1)]);
-              else
-                v[h][4 * i + q] = __uint_as_float(x) * f[0];
+              else if (q & 1)   // two at a time: the same roundings
+                mul_x2(v[h][4 * i + q - 1], v[h][4 * i + q], __uint_as_float(r[h][4 * i + q - 1]), __uint_as_float(x), f[0]);
             }
         }
         uint32_t o[16];   // the block's packed pairs, in stmatrix order
@@ -907,6 +960,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
     if (lane == 0) bulk_wait_read<0>();
   }
 
+  if (p.late_wait) pdl_wait();
   tc_fence_before();
   if constexpr (kPair || kSplit) cluster_sync();  // no CTA leaves while another still signals or writes it
   else cta_sync();

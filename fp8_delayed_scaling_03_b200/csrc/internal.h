@@ -192,6 +192,11 @@ struct GroupedParams {
   SideWrites side;
   RingFinalize fin[2];
   int nfin;
+  // Set for a launch that does not depend on the one before it (a product of
+  // this kernel too): it starts while that one still runs, since by then every
+  // CTA there has seen all earlier work complete, and waits for it before its
+  // own end, so that what follows may rely on both.
+  int late_wait;
   const float* sw_src;        // per-group scale snapshot: sw_dst[i] = sw_src[i], i < sw_n
   float* sw_dst;
   int sw_n;
