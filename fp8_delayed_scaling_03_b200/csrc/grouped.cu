@@ -936,17 +936,49 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
                   }
                 }
               }
-            } else if (n0 + lane < p.nlane) {
-              // rows that 16-byte stores cannot address: a lane per output
-              // column (4-byte stores of pairs from the first even address on,
-              // with the odd ends apart, took a third longer)
-              unsigned short* dst = dh + static_cast<int64_t>(c0) * p.ldd + n0 + lane;
-              #pragma unroll 8
-              for (int c = 0; c < 32; ++c) {
-                const unsigned short x = *reinterpret_cast<const unsigned short*>(
-                    buf + c * 128 + (((chunk0 + (lane >> 3)) ^ (c & 7)) * 16) + (lane & 7) * 2);
-                if (c < live) dst[static_cast<int64_t>(c) * p.ldd] = x;
+            } else {
+              // Rows that 16-byte stores cannot address.  Each of the two
+              // warps takes every other column, all 64 lanes of it, so that
+              // its rows start alike -- at an even address or an odd one --
+              // whatever the row pitch: 4-byte stores from the first even
+              // address on, the two odd ends of all its rows in one more.
+              const int nd = n0 - (qd & 1) * 32, left = p.nlane - nd;   // the slab's first lane, lanes from there
+              unsigned short* const dst = dh + static_cast<int64_t>(c0 + (qd & 1)) * p.ldd + nd;
+              const int64_t pitch = 2 * p.ldd;
+              const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
+              auto at = [&](int c, int j) {
+                return buf + c * 128 + (((j >> 3) ^ (c & 7)) * 16) + (j & 7) * 2;
+              };
+              const int j = 2 * lane + shift;
+              const int j1 = min(j + 1, 63);
+              const bool pair = j + 1 < min(left, 64), single = !pair && j < left;   // (single: an odd row's or D's last lane)
+              #pragma unroll 1
+              for (int i0 = 0; i0 < 16; i0 += 8) {
+                // eight rows' pairs, then their stores: no store waits for a
+                // load (one row at a time took twice as long)
+                uint32_t x[8];
+                if (shift) {
+                  #pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const int c = 2 * (i0 + i) + (qd & 1);
+                    x[i] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(at(c, j))) |
+                           static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(at(c, j1))) << 16;
+                  }
+                } else {
+                  #pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(at(2 * (i0 + i) + (qd & 1), j));
+                }
+                unsigned short* to = dst + i0 * pitch + j;
+                #pragma unroll
+                for (int i = 0; i < 8; ++i, to += pitch) {
+                  if (2 * (i0 + i) + (qd & 1) < live) {
+                    if (pair) *reinterpret_cast<uint32_t*>(to) = x[i];
+                    if (single) *to = static_cast<unsigned short>(x[i]);
+                  }
+                }
               }
+              if (shift && lane < 16 && 2 * lane + (qd & 1) < live && left > 0)
+                dst[lane * pitch] = *reinterpret_cast<const unsigned short*>(at(2 * lane + (qd & 1), 0));
             }
             __syncwarp();
           }
