@@ -800,8 +800,13 @@ def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch
 @dataclass
 class Int8Result:
     y: torch.Tensor
-    x8: torch.Tensor
+    codes: torch.Tensor   # x8 with its rows' padding
     sx: torch.Tensor
+    cols: int
+
+    @property
+    def x8(self) -> torch.Tensor:
+        return self.codes[:, : self.cols]
 
 
 def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) -> Int8Result:
@@ -828,8 +833,6 @@ def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) 
     if x8 is None:
         ldx8 = (K + 15) // 16 * 16
         x8 = x.new_empty(M, ldx8, dtype=torch.int8)
-        if ldx8 != K:
-            x8 = x8[:, :K]
     else:
         ldx8 = _matrix(_out(x8, (M, K), torch.int8, x, "x8"), "x8")[2]
     if sx is None:
@@ -839,4 +842,4 @@ def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) 
     _call("fp8_linear_int8_forward", dev, _call_linear_int8,
           _pack_int8(M, N, K, x.data_ptr(), x_dtype, ldx, w8.data_ptr(), ldw, sw.data_ptr(), _address(bias), bias_dtype,
                      x8.data_ptr(), ldx8, sx.data_ptr(), y.data_ptr(), y_dtype, ldy))
-    return Int8Result(y, x8, sx)
+    return Int8Result(y, x8, sx, K)

@@ -882,13 +882,16 @@ int validate_groups(const fp8_groups* g) {
 }
 
 constexpr int64_t kMaxTiles = int64_t(1) << 30;
+// Sizes leave 32-bit coordinates room for a tile past the end.
+constexpr int64_t kMaxGroupedDim = kMaxDim - 1024;
 
 // Checks a grouped product and turns it into a kernel call.  The weight (or,
 // for a ragged contraction, X: the operand along D's contiguous axis) is the
 // lane operand, which is fp8_mm's B in both forms.
 int grouped_call(const fp8_mm_args& a, int ragged, const fp8_groups& g, GroupedCall* out) {
   if (ragged != FP8_RAGGED_M && ragged != FP8_RAGGED_K) return FP8_ERR_INVALID_ARG;
-  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > kMaxDim || a.n > kMaxDim || a.k > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > kMaxGroupedDim || a.n > kMaxGroupedDim || a.k > kMaxGroupedDim)
+    return FP8_ERR_INVALID_ARG;
   if (!is_fmt(a.fmt_a) || !is_fmt(a.fmt_b) || !a.scale_a || !a.scale_b) return FP8_ERR_INVALID_ARG;
   if ((a.a_major != FP8_K_MAJOR && a.a_major != FP8_MN_MAJOR) || (a.b_major != FP8_K_MAJOR && a.b_major != FP8_MN_MAJOR))
     return FP8_ERR_INVALID_ARG;
@@ -969,7 +972,8 @@ int run_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, 
 }
 
 int int8_call(const fp8_mm_int8_args& a, GroupedCall* out) {
-  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > kMaxDim || a.n > kMaxDim || a.k > kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (a.m < 0 || a.n < 0 || a.k < 0 || a.m > kMaxGroupedDim || a.n > kMaxGroupedDim || a.k > kMaxGroupedDim)
+    return FP8_ERR_INVALID_ARG;
   if (a.k > FP8_MAX_INT8_K) return FP8_ERR_TOO_LARGE;
   if (!is_wide(a.d_dtype)) return FP8_ERR_INVALID_ARG;
   if (a.bias && (!is_wide(a.bias_dtype) || !aligned(a.bias, esize(a.bias_dtype)))) return FP8_ERR_INVALID_ARG;

@@ -39,6 +39,7 @@
 // cannot clip: the next group's rows follow) leaves as 16-byte stores guarded
 // by that end, and one of rows that TMA cannot address as single elements.
 #include <algorithm>
+#include <atomic>
 
 #include "device.cuh"
 #include "internal.h"
@@ -1007,7 +1008,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
 template <bool kInt8, bool kRaggedK, bool kPair, bool kSplit, int OUT>
 cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_t max_tiles, int dev, int sms,
                          cudaStream_t s) {
-  static int capacity[64] = {};   // CTAs (pairs) that can be resident at once; 0: not yet configured
+  static std::atomic<int> capacity[64];   // CTAs (pairs) that can be resident at once; 0: not yet configured
   auto kernel = grouped_kernel<kInt8, kRaggedK, kPair, kSplit, OUT>;
   const int per_unit = kPair ? 2 : (kSplit ? p.split : 1);
   cudaLaunchConfig_t cfg = {};
@@ -1036,7 +1037,7 @@ cudaError_t launch_build(const CUtensorMap* maps, const GroupedParams& p, int64_
     capacity[dev] = fit;
   }
   // a split launch has a cluster for every tile there can be: each runs one
-  const int64_t units = kSplit ? max_tiles : std::min<int64_t>(capacity[dev], max_tiles);
+  const int64_t units = kSplit ? max_tiles : std::min<int64_t>(capacity[dev].load(), max_tiles);
   cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, units) * per_unit));
   cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
   cfg.attrs = attr;

@@ -283,8 +283,8 @@ FP8LIN_API int fp8_mm_batched(const fp8_mm_args* args, int64_t batch, int64_t st
  *     e} A(i,r) B(j,r)) / (scale_a * scale_b[...]) ), the weight gradient
  *     dW_e = G_e^T X_e.  args->k is the number of rows of the A and B buffers,
  *     both MN-major; D_e = d + e * stride_d, zero for an empty group.
- * The other majors, a bias and a forced tile_cfg (FP8_TILE_AUTO only) are
- * FP8_ERR_UNSUPPORTED.  One launch, no workspace, deterministic; a row's
+ * Sizes are at most 2^31 - 1025.  The other majors, a bias and a forced
+ * tile_cfg (FP8_TILE_AUTO only) are FP8_ERR_UNSUPPORTED.  One launch, no workspace, deterministic; a row's
  * result does not depend on the other groups' rows. */
 #define FP8_MAX_GROUPS 1024
 typedef enum { FP8_RAGGED_M = 0, FP8_RAGGED_K = 1 } fp8_ragged;
@@ -315,7 +315,7 @@ FP8LIN_API int fp8_quantize_int8(const void* in, int in_dtype, int64_t rows, int
 
 /* D[i, j] = round( ((float)(sum_k A[i,k] B[j,k]) * scale_a[i]) * scale_b[j] + bias[j] )
  * The sum is exact in int32 (tcgen05, kind::i8); k > FP8_MAX_INT8_K could
- * overflow it and returns FP8_ERR_TOO_LARGE.  Its conversion and the two
+ * overflow it and returns FP8_ERR_TOO_LARGE.  m and n are at most 2^31 - 1025.  Its conversion and the two
  * products are each rounded to fp32, then the one rounding to D's type.
  *   a        int8 [m, lda], b int8 [n, ldb]: both K-major, ld % 16 == 0, base
  *            16-byte aligned (as the fp8 matrices)

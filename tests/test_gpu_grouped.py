@@ -367,6 +367,59 @@ def test_capture_streams_and_repeats():
     assert F.fp8_get_device_status() == 0
 
 
+def test_one_weight_for_all_groups():
+    """stride_b 0: every group uses the same weight, with scales of their own."""
+    c, n, k = [40, 0, 90], 176, 112
+    rows = sum(c)
+    x8, w8, sx, sw, off = codes(rows, k, 0, 1), codes(n, k, 0, 2), scales(1, 3), scales(3, 4), offsets_of(c)
+    y = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    a = F.MmArgs(rows, n, k, x8.data_ptr(), 0, 0, x8.stride(0), w8.data_ptr(), 0, 0, w8.stride(0), sx.data_ptr(),
+                 sw.data_ptr(), None, 0, None, y.data_ptr(), n, 0, None, 0)
+    F.fp8_mm_grouped(a, F.FP8_RAGGED_M, F.Groups(3, off.data_ptr(), 0, 0, 0, 1), y.device)
+    three = torch.zeros(3, n, w8.stride(0), dtype=torch.uint8, device="cuda")
+    three[:, :, :k] = w8
+    assert torch.equal(y, F.grouped_mm(x8, three[:, :, :k], off, sx, sw))
+
+
+def test_weight_gradient_scales_and_pitches():
+    """Through the C entry: one scale per group, and D with a row pitch and a gap between the groups."""
+    c, n, k = [33, 0, 64, 7], 130, 72
+    rows, ld, gap = sum(c), 80, 130 * 80 + 48
+    x8, g8, sg, sx, off = codes(rows, k, 0, 1), codes(rows, n, 1, 2), scales(1, 3), scales(4, 4), offsets_of(c)
+    buf = torch.full((4 * gap,), 3.0, dtype=torch.bfloat16, device="cuda")
+    a = F.MmArgs(n, k, rows, g8.data_ptr(), 1, 1, g8.stride(0), x8.data_ptr(), 0, 1, x8.stride(0), sg.data_ptr(),
+                 sx.data_ptr(), None, 0, None, buf.data_ptr(), ld, 0, None, 0)
+    F.fp8_mm_grouped(a, F.FP8_RAGGED_K, F.Groups(4, off.data_ptr(), 0, 0, gap, 1), buf.device)
+    at = 0
+    for e, m in enumerate(c):
+        x, g, s = value(x8[at:at + m], 0), value(g8[at:at + m], 1), float(sg) * float(sx[e])
+        d = buf[e * gap:e * gap + n * ld].view(n, ld)
+        assert_close(d[:, :k], g.t() @ x / s, g.abs().t() @ x.abs() / s, e)
+        assert bool((d[:, k:] == 3.0).all()) and bool((buf[e * gap + n * ld:(e + 1) * gap] == 3.0).all())
+        at += m
+
+
+def test_weights_and_gradients_past_31_bits():
+    """Weights of more than 2^31 bytes, and a weight gradient of more than 2^31 elements."""
+    E, n, k = 9, 16384, 16640
+    assert E * n * k > 2 ** 31
+    c = [3, 0, 40, 1, 0, 0, 2, 0, 18]
+    rows = sum(c)
+    off = offsets_of(c)
+    w8 = torch.randint(0, 0x40, (E, n, k), dtype=torch.uint8, device="cuda")
+    x8, g8, sx, sg = codes(rows, k, 0, 1), codes(rows, n, 1, 2), scales(1, 3), scales(1, 4)
+    b = F.grouped_linear_backward(g8, F.ForwardResult(None, x8, w8, sx, sx, None, None), off, None, g_scale_in=sg)
+    y = F.grouped_mm(x8, w8, off, sx, sx)
+    e = 8
+    x, g, w = value(x8[46:], 0), value(g8[46:], 1), value(w8[e], 0)
+    s, sd, sdw = float(sx) ** 2, float(sg) * float(sx), float(sg) * float(sx)
+    assert_close(y[46:], x @ w.t() / s, x.abs() @ w.abs().t() / s, "y")
+    assert_close(b.dx[46:], g @ w / sd, g.abs() @ w.abs() / sd, "dx")
+    at = slice(n - 300, n)
+    assert_close(b.dw[e, at], g[:, at].t() @ x / sdw, g[:, at].abs().t() @ x.abs() / sdw, "dw")
+    assert bool((b.dw[7, at] == 0).all())
+
+
 def test_column_offsets_past_31_bits():
     """Rows of y beyond 2^31 elements."""
     n, k, rows = 11008, 16, 200_000

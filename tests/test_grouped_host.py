@@ -37,7 +37,7 @@ def test_grouped_refusals(fp8):
     bad, mis, uns, big = E.FP8_ERR_INVALID_ARG, E.FP8_ERR_MISALIGNED, E.FP8_ERR_UNSUPPORTED, E.FP8_ERR_TOO_LARGE
     assert fp8._lib.fp8_mm_grouped(None, 0, None, None) == bad
     for ragged in (0, 1):
-        for kw in (dict(m=-1), dict(n=1 << 31), dict(k=-5), dict(fmt_a=2), dict(fmt_b=-1), dict(scale_a=None),
+        for kw in (dict(m=-1), dict(n=1 << 31), dict(n=(1 << 31) - 1), dict(k=-5), dict(fmt_a=2), dict(fmt_b=-1), dict(scale_a=None),
                    dict(scale_b=None), dict(a_major=7), dict(a=None), dict(b=None), dict(lda=100), dict(ldb=112),
                    dict(d=None), dict(ldd=127), dict(d=A + 1)):
             assert grouped(fp8, ragged, **kw) == bad, (ragged, kw)
@@ -78,7 +78,7 @@ def int8(fp8, **kw):
 def test_int8_refusals(fp8):
     E = fp8
     assert fp8._lib.fp8_mm_int8(None, None) == E.FP8_ERR_INVALID_ARG
-    for kw in (dict(m=-1), dict(n=-1), dict(k=-1), dict(m=1 << 31), dict(a=None), dict(b=None), dict(lda=48), dict(ldb=48),
+    for kw in (dict(m=-1), dict(n=-1), dict(k=-1), dict(m=1 << 31), dict(m=(1 << 31) - 1024), dict(a=None), dict(b=None), dict(lda=48), dict(ldb=48),
                dict(scale_a=None), dict(scale_b=None), dict(scale_a=A + 2), dict(scale_b=A + 1), dict(d=None), dict(ldd=31),
                dict(d=A + 1), dict(d=A + 2, d_dtype=2), dict(d_dtype=3), dict(d_dtype=-1), dict(bias=A, bias_dtype=3),
                dict(bias=A + 1), dict(bias=A + 2, bias_dtype=2)):
