@@ -564,13 +564,17 @@ _call_grouped_backward = _packed_call("fp8_linear_grouped_backward", _B, _B, _P)
 _call_linear_int8 = _packed_call("fp8_linear_int8_forward", _B, _P)
 
 
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _call(where: str, dev: int, fn, *args) -> None:
     """fn on the current stream of device `dev`, which is made current for the call."""
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if _current_device() == dev:
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            status = fn(*args, _raw_stream(dev))
     if status != FP8_OK:
         raise Fp8Error(status, where)
 
@@ -584,6 +588,9 @@ def _one_device(first: torch.Tensor, *others: torch.Tensor | None) -> int:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
     return dev
+
+
+_FP32 = torch.float32
 
 
 def _address(t: torch.Tensor | None) -> int:
@@ -622,15 +629,17 @@ def _offsets(t: torch.Tensor) -> tuple[int, int]:
 
 def _scale_step(scale: torch.Tensor, groups: int, what: str) -> int:
     n = scale.numel()
-    if scale.dtype != torch.float32 or not scale.is_contiguous() or (n != 1 and n != groups):
+    if scale.dtype is not _FP32 or (n != 1 and n != groups) or not scale.is_contiguous():
         raise ValueError(f"{what}: a contiguous fp32 tensor of 1 or {groups} scales")
     return int(n != 1)
 
 
 def _codes_fmt(t: torch.Tensor, fmt: int, what: str) -> None:
     """fp8 codes of format fmt: uint8, or the float8 type of that format."""
+    if t.dtype is torch.uint8:
+        return
     held = _CODE_TYPES.get(t.dtype, -1)
-    if held is not None and held != fmt:
+    if held != fmt:
         raise ValueError(f"{what}: expected fp8 codes of format {fmt}, got {t.dtype}")
 
 
@@ -676,7 +685,7 @@ def grouped_mm(x8, w8, offsets, sx, sw, y=None, fmt_x=FP8_E4M3, fmt_w=FP8_E4M3, 
         raise ValueError(f"x8 and w8 of one contraction length: {tuple(x8.shape)}, {tuple(w8.shape)}")
     _codes_fmt(x8, fmt_x, "x8")
     _codes_fmt(w8, fmt_w, "w8")
-    if sx.numel() != 1 or sx.dtype != torch.float32:
+    if sx.numel() != 1 or sx.dtype is not _FP32:
         raise ValueError("sx: one fp32 scale")
     step = _scale_step(sw, groups, "sw")
     dev = _one_device(x8, w8, offsets, sx, sw, y)
@@ -743,7 +752,7 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
         raise ValueError(f"g {tuple(g.shape)}, x8 {tuple(x8.shape)} and w8 {tuple(w8.shape)} do not fit")
     _codes_fmt(x8, fmt_x, "x8")
     _codes_fmt(w8, fmt_w, "w8")
-    if sx.numel() != 1 or sx.dtype != torch.float32:
+    if sx.numel() != 1 or sx.dtype is not _FP32:
         raise ValueError("sx: one fp32 scale")
     step = _scale_step(sw, groups, "sw")
     gd, gq = _operand_dtype(g, fmt_g)
