@@ -744,14 +744,19 @@ int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile, int64_t tile_l
 //   the same with its k-blocks split over a cluster of 2 .. 4 CTAs (few tiles
 //   and a long contraction);
 //   a CTA pair, 256 lanes x 256 columns,
-// by the time of the most loaded CTA: waves x (k-blocks x time of one +
-// epilogue), with the times in microseconds measured on a B200: a k-block of
-// up to 32 columns 0.20, 64 0.24, 128 0.31, 256 columns 0.37 on one CTA as on a
-// pair; an epilogue step (32 columns, two at a time) 0.33; joining split sums
-// 1.0.  Group sizes are not known here: a group is taken to be a quarter
-// larger than the average.  Where the weights' bytes bound the time the
-// choices hardly differ, and the smallest tile, which loads the fewest tokens,
-// comes first.
+// by the time of the most loaded CTA, whose tiles' main loops and outputs
+// overlap: main + output + (waves - 1) max(main + 0.25, output).  The times, in
+// microseconds, are fitted to a B200 (24 shapes of 1 to 5000 rows, 1 to 64
+// groups, every choice timed; the rule's is within 3 % of the best for 19 of
+// them, 14 % at most):
+//   a k-block of up to 32 columns 0.17, 64 0.21, 128 0.25, 256 0.36 on one CTA
+//   as on a pair; an output 1.0 + 0.3 for each two 32-column steps (0.95 where
+//   D's rows cannot take 16-byte stores); joining s partial sums
+//   0.9 + (s - 1) (0.4 + 0.5 (t / 64)^2).
+// Group sizes are not known here: a group is taken to need half a tile more
+// than its average rows fill, one at least.  Where the weights' bytes bound
+// the time the choices hardly differ, and the smallest tile, which loads the
+// fewest tokens, comes first.
 void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair, int* split) {
   const int64_t tl = (c.nlane + 127) / 128, tl2 = (c.nlane + 255) / 256;
   *split = 1;
@@ -761,21 +766,26 @@ void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair, int
     if (!*pair) *tile = 128;
     return;
   }
-  const int64_t live = std::max<int64_t>(1, std::min(c.groups, c.rows));
-  const double rows = c.groups == 1 ? static_cast<double>(c.rows)
-                                    : std::max(1.0, 1.25 * static_cast<double>(c.rows) / static_cast<double>(live));
+  const double live = static_cast<double>(std::max<int64_t>(1, std::min(c.groups, c.rows)));
+  const double avg = static_cast<double>(c.rows) / live;
   const int64_t kb = (c.k + 127) / 128;
-  auto col_tiles = [&](int64_t t) { return static_cast<int64_t>(std::ceil(rows / static_cast<double>(t))) * live; };
-  auto waves = [&](int64_t units, int64_t slots) { return static_cast<double>((units + slots - 1) / slots); };
+  const bool wide = aligned(c.d, 16) && (c.ldd * esize(c.d_dtype)) % 16 == 0;
+  auto col_tiles = [&](double t) { return c.groups == 1 ? std::ceil(avg / t) : live * std::max(1.0, avg / t + 0.5); };
+  auto time = [&](double units, int slots, int64_t blocks, double t_kb, int64_t t) {
+    const double main = t_kb * static_cast<double>(blocks);
+    const double out = 1.0 + static_cast<double>((t + 63) / 64) * (wide ? 0.3 : 0.95);
+    return main + out + (std::ceil(units / std::max(1, slots)) - 1.0) * std::max(main + 0.25, out);
+  };
   *pair = true;
-  double best = waves(col_tiles(256) * tl2, std::max(1, sms / 2)) * (0.37 * static_cast<double>(kb) + 4 * 0.33);
+  double best = time(col_tiles(256) * static_cast<double>(tl2), sms / 2, kb, 0.36, 256);
   for (int64_t t = 16; t <= 256; t *= 2) {
-    const double t_kb = t <= 32 ? 0.20 : (t == 64 ? 0.24 : (t == 128 ? 0.31 : 0.37));
-    const double epilogue = 0.33 * static_cast<double>((t + 63) / 64);
+    const double t_kb = t <= 32 ? 0.17 : (t == 64 ? 0.21 : (t == 128 ? 0.25 : 0.36));
+    const double tiles = col_tiles(static_cast<double>(t)) * static_cast<double>(tl);
     for (int64_t s = 1; s <= 4; ++s) {
-      if (s > 1 && (t > 128 || s * 4 > kb || (s - 1) * t > 192 || col_tiles(t) * tl * s > sms)) break;
-      const double us = waves(col_tiles(t) * tl * s, sms) * (t_kb * static_cast<double>((kb + s - 1) / s) + epilogue) +
-                        (s > 1 ? 1.0 : 0.0);
+      if (s > 1 && (t > 128 || s * 4 > kb || (s - 1) * t > 192 || tiles * static_cast<double>(s) > sms)) break;
+      const double n = static_cast<double>(s - 1), q = static_cast<double>(t) / 64.0;
+      const double us = time(tiles * static_cast<double>(s), sms, (kb + s - 1) / s, t_kb, t) +
+                        (s > 1 ? 0.9 + n * (0.4 + 0.5 * q * q) : 0.0);
       if (us < best * 0.999) {
         best = us;
         *pair = false;
