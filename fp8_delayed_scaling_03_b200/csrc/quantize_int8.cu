@@ -11,11 +11,8 @@
 // a second time, from L2).  The maximum is taken over the absolute values' bit
 // patterns, which order like the values and put infinities and NaN on top.
 //
-// The cast multiplies by 127 / amax in fp32: two roundings, at most 1.6e-5 off
-// for |t| <= 127.  Only a value that close to the border of two codes can come
-// out wrong, so for those (one in some 25,000) 254 |x| is compared with
-// (2 k + 1) amax, which 64 bits hold exactly.  Codes therefore depend on the
-// values alone, not on how the quotient is computed.
+// Codes depend on the values alone, not on how the quotient is computed: see
+// cast_chunk().
 #include <type_traits>
 
 #include "device.cuh"
@@ -29,8 +26,8 @@ constexpr int kChunk = 16;     // elements per 16-byte store of codes
 constexpr int kHeld = 2;       // chunks a thread keeps in registers
 constexpr int kMaxThreads = 512;  // 128 registers a thread
 constexpr float kBorder = 0.5f - 2e-5f;
-constexpr float kTinyAmax = 1e-36f;   // 127 / kTinyAmax is below the largest float
-constexpr float kUp = 1.2676506002282294e30f;  // 2^100
+constexpr float kTinyAmax = 1e-36f, kHugeAmax = 1e36f;   // between them 127 / amax and 127 amax are finite
+constexpr float k2p100 = 1.2676506002282294e30f;
 
 template <typename T>
 struct Chunk {
@@ -72,41 +69,121 @@ __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int64_t col, int64_
   return c;
 }
 
+// The running maximum of the absolute values' bit patterns: of 2-byte types
+// two to a word.
 template <typename T>
 __device__ __forceinline__ uint32_t chunk_max(const Chunk<T>& c, uint32_t m) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(c.w);
   #pragma unroll
-  for (int j = 0; j < kChunk; ++j) m = max(m, __float_as_uint(value<T>(c, j)) & 0x7FFFFFFFu);
+  for (int j = 0; j < 4 * static_cast<int>(sizeof(T)); ++j) {
+    if constexpr (sizeof(T) == 2) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+    else m = max(m, w[j] & 0x7FFFFFFFu);
+  }
   return m;
 }
 
-// 16 codes.  kTiny: amax is so small that 127 / amax overflows; values and amax
-// are then taken times 2^100, which is exact.
-template <typename T, bool kTiny>
-__device__ __forceinline__ uint4 cast_chunk(const Chunk<T>& c, float amax) {
-  // t + 1.5 * 2^23 rounds t to the nearest integer (ties to even) and holds it
-  // in its low bits, two's complement
+// ... as the bit pattern of an fp32 value (infinities and NaN: that of
+// infinity or above).
+template <typename T>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m) {
+  if constexpr (sizeof(T) == 4) return m;
+  const uint32_t h = max(m & 0xFFFFu, m >> 16);
+  if constexpr (std::is_same<T, __half>::value)
+    return h >= 0x7C00u ? 0x7F800000u : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
+  else return h << 16;
+}
+
+// Two fp32 values in one register pair and the packed operations on them.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint2 bits2(uint64_t v) {
+  uint2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// What the casts of one row share.  A row whose amax is so small that 127 /
+// amax overflows is taken times 2^100, one so large that 127 amax does times
+// 2^-100: exact for every value that can get another code than 0.
+struct RowScale {
+  float up, top, inv;          // 1, 2^100 or 2^-100; amax up; 127 / top
+  bool zero;                   // all codes 0
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t bits) {
+  RowScale s;
+  s.zero = bits == 0u || bits >= 0x7F800000u;
+  const float amax = s.zero ? 1.0f : __uint_as_float(bits);
+  s.up = amax < kTinyAmax ? k2p100 : (amax > kHugeAmax ? 1.0f / k2p100 : 1.0f);
+  s.top = amax * s.up;
+  s.inv = __fdiv_rn(127.0f, s.top);
+  return s;
+}
+
+// The 16 codes of a chunk.  kScaled: s.up is not 1.
+//
+// m = the integer nearest to t = v inv, by adding and subtracting 1.5 * 2^23,
+// whose sum holds it in its low bits, two's complement.  t is off by at most
+// 1.6e-5, so m is wrong only next to the border of two codes:
+//   2-byte inputs: 127 v and the remainder r = 127 v - m top are exact in
+//     fp32, so |r| against top / 2 tells, and a tie goes to the even code.
+//     Ties are common there (bf16 values and amax have 8 significant bits):
+//     one in some 200, so every element is corrected, without a branch (a
+//     branch an element took a third longer).  The comparison adds m's lowest
+//     bit to r's pattern: above top / 2, or equal to it and m odd.
+//   fp32 inputs: only where t is within 2e-5 of a border, 254 |v| is compared
+//     with (2 k + 1) top, which 64 bits hold exactly (one in some 25,000).
+template <typename T, bool kScaled>
+__device__ __forceinline__ uint4 cast_chunk(const Chunk<T>& c, const RowScale& s) {
   constexpr float kMagic = 12582912.0f;
-  const float top = kTiny ? amax * kUp : amax;
-  const float inv = __fdiv_rn(127.0f, top);
-  auto scaled = [&](int j) { return kTiny ? value<T>(c, j) * kUp : value<T>(c, j); };
   uint32_t q[kChunk];
-  bool near = false;
-  #pragma unroll
-  for (int j = 0; j < kChunk; ++j) {
-    const float t = __fmul_rn(scaled(j), inv);
-    const float m = __fadd_rn(t, kMagic);
-    q[j] = __float_as_uint(m);
-    near = near || fabsf(__fsub_rn(t, __fsub_rn(m, kMagic))) > kBorder;
-  }
-  if (near) {
+  if constexpr (sizeof(T) == 2) {
+    const uint64_t inv = f2(s.inv, s.inv), up = f2(s.up, s.up), magic = f2(kMagic, kMagic), minus = f2(-kMagic, -kMagic),
+                   c127 = f2(127.0f, 127.0f), ntop = f2(-s.top, -s.top);
+    const uint32_t half = __float_as_uint(0.5f * s.top);
+    #pragma unroll
+    for (int j = 0; j < kChunk; j += 2) {
+      uint64_t v = f2(value<T>(c, j), value<T>(c, j + 1));
+      if (kScaled) v = mul2(v, up);
+      const uint64_t m = add2(mul2(v, inv), magic);
+      const uint2 r = bits2(fma2(add2(m, minus), ntop, mul2(v, c127)));
+      const uint2 b = bits2(m);
+      auto code = [&](uint32_t mb, uint32_t rb) {
+        const uint32_t a = rb + (mb & 1u);
+        if (static_cast<int>(a) > static_cast<int>(half)) mb += 1u;   // r > 0
+        if (a > (half | 0x80000000u)) mb -= 1u;                       // r < 0
+        return mb;
+      };
+      q[j] = code(b.x, r.x);
+      q[j + 1] = code(b.y, r.y);
+    }
+  } else {
     #pragma unroll
     for (int j = 0; j < kChunk; ++j) {
-      const float v = scaled(j), t = __fmul_rn(v, inv);
-      if (fabsf(t - rintf(t)) > kBorder) {
-        // |t| is within 1.6e-5 of k + 0.5: which side 127 |v| / top lies on,
-        // from two products that 64 bits hold exactly
+      const float v = kScaled ? value<T>(c, j) * s.up : value<T>(c, j), t = __fmul_rn(v, s.inv);
+      const float m = __fadd_rn(t, kMagic);
+      q[j] = __float_as_uint(m);
+      if (fabsf(__fsub_rn(t, __fsub_rn(m, kMagic))) > kBorder) {
         const int k = static_cast<int>(fabsf(t));
-        const double lhs = 254.0 * static_cast<double>(fabsf(v)), rhs = static_cast<double>(2 * k + 1) * static_cast<double>(top);
+        const double lhs = 254.0 * static_cast<double>(fabsf(v)), rhs = static_cast<double>(2 * k + 1) * static_cast<double>(s.top);
         const int a = lhs > rhs || (lhs == rhs && (k & 1)) ? k + 1 : k;
         q[j] = static_cast<uint32_t>(v < 0.0f ? -a : a);
       }
@@ -119,12 +196,10 @@ __device__ __forceinline__ uint4 cast_chunk(const Chunk<T>& c, float amax) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The codes of a chunk of a row whose largest magnitude has the given bits.
 template <typename T>
-__device__ __forceinline__ uint4 codes(const Chunk<T>& c, uint32_t bits) {
-  if (bits == 0u || bits >= 0x7F800000u) return make_uint4(0u, 0u, 0u, 0u);
-  const float amax = __uint_as_float(bits);
-  return amax < kTinyAmax ? cast_chunk<T, true>(c, amax) : cast_chunk<T, false>(c, amax);
+__device__ __forceinline__ uint4 codes(const Chunk<T>& c, const RowScale& s) {
+  if (s.zero) return make_uint4(0u, 0u, 0u, 0u);
+  return s.up == 1.0f ? cast_chunk<T, false>(c, s) : cast_chunk<T, true>(c, s);
 }
 
 // blockDim.y rows a block, blockDim.x threads a row (one warp when there is
@@ -149,7 +224,7 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_int8_kernel(const Int8Qu
     if (tid + i * step < chunks) bits = chunk_max<T>(held[i], bits);
   for (int64_t c = tid + kHeld * step; c < chunks; c += step)
     bits = chunk_max<T>(load_chunk<T>(row, c * kChunk, p.cols, p.vec_ok), bits);
-  bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+  bits = __reduce_max_sync(0xFFFFFFFFu, max_bits<T>(bits));
   if (blockDim.y == 1) {
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = bits;
     __syncthreads();
@@ -159,14 +234,15 @@ __global__ void __launch_bounds__(kMaxThreads) quantize_int8_kernel(const Int8Qu
   if (live && tid == 0)
     p.scale[r] = bits >= 0x7F800000u ? __uint_as_float(0x7FFFFFFFu)
                                      : (bits ? __fdiv_rn(__uint_as_float(bits), 127.0f) : 1.0f);
+  const RowScale rs = row_scale(bits);
   int8_t* out = p.out + (live ? r : 0) * p.ld_out;
   #pragma unroll
   for (int i = 0; i < kHeld; ++i)
     if (tid + i * step < chunks)
-      *reinterpret_cast<uint4*>(out + (tid + i * step) * kChunk) = codes<T>(held[i], bits);
+      *reinterpret_cast<uint4*>(out + (tid + i * step) * kChunk) = codes<T>(held[i], rs);
   for (int64_t c = tid + kHeld * step; c < chunks; c += step)
     *reinterpret_cast<uint4*>(out + c * kChunk) =
-        codes<T>(load_chunk<T>(row, c * kChunk, p.cols, p.vec_ok), bits);
+        codes<T>(load_chunk<T>(row, c * kChunk, p.cols, p.vec_ok), rs);
 }
 
 }  // namespace
