@@ -844,6 +844,7 @@ int run_grouped(const GroupedCall& c, cudaStream_t st, const SideWrites* side = 
   p.k_blocks = static_cast<int>(((c.ragged_k ? c.rows : c.k) + 127) / 128);
   p.lane_shared = c.stride_lane == 0 ? 1 : 0;
   p.col_tile = tile;
+  while ((1 << p.col_shift) < tile) ++p.col_shift;
   p.split = split;
   grouped_smem(&p, pair);
   p.lane_mn = c.lane_mn;

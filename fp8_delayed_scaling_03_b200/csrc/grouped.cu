@@ -263,13 +263,20 @@ __device__ __forceinline__ Tile token_tile(const GroupedParams& p, const int* bo
   w.e = lo;
   t -= first[lo];
   const int row0 = bound[lo], rows = bound[lo + 1] - row0;
-  const int tiles_col = (rows + p.col_tile - 1) / p.col_tile;
-  const int per = kRaster * p.tiles_lane;
-  const int g = t / per;
-  const int gc = min(kRaster, tiles_col - g * kRaster);
-  t -= g * per;
-  const int tc = g * kRaster + t % gc;
-  w.lane0 = (t / gc) * kTileLanes;
+  const int tiles_col = (rows + p.col_tile - 1) >> p.col_shift;
+  int tc = 0, tl = t;
+  if (tiles_col > 1) {   // (divisions are in the way of the first loads of a small launch)
+    int base = 0;
+    if (tiles_col > kRaster) {
+      const int per = kRaster * p.tiles_lane, g = t / per;
+      t -= g * per;
+      base = g * kRaster;
+    }
+    const int gc = min(kRaster, tiles_col - base);
+    tl = t / gc;
+    tc = base + t - tl * gc;
+  }
+  w.lane0 = tl * kTileLanes;
   w.col0 = row0 + tc * p.col_tile;
   w.cols = min(p.col_tile, row0 + rows - w.col0);
   w.k0 = 0;
@@ -337,7 +344,7 @@ __device__ __forceinline__ void scan_groups(const GroupedParams& p, int* bound, 
       bound[0] = 0;
       bound[1] = p.rows;
       first[0] = 0;
-      first[1] = kRaggedK ? p.tiles_lane * p.tiles_col : (p.rows + p.col_tile - 1) / p.col_tile * p.tiles_lane;
+      first[1] = kRaggedK ? p.tiles_lane * p.tiles_col : ((p.rows + p.col_tile - 1) >> p.col_shift) * p.tiles_lane;
     }
     return;
   }
@@ -346,6 +353,9 @@ __device__ __forceinline__ void scan_groups(const GroupedParams& p, int* bound, 
                               : static_cast<int64_t>(__ldcg(static_cast<const int*>(p.offsets) + i));
     return static_cast<int>(min(max(v, static_cast<int64_t>(0)), static_cast<int64_t>(p.rows)));
   };
+  // (the loads of a round are issued before the round that precedes it is
+  // scanned: one trip to L2 for up to 32 groups)
+  int ahead = lane < p.groups ? offset(lane + 1) : 0;
   top = offset(0);
   if (lane == 0) {
     bound[0] = top;
@@ -353,29 +363,37 @@ __device__ __forceinline__ void scan_groups(const GroupedParams& p, int* bound, 
   }
   for (int e0 = 0; e0 < p.groups; e0 += 32) {
     const int e = e0 + lane;
-    int end = e < p.groups ? offset(e + 1) : 0;
-    #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, end, d);
-      if (lane >= d) end = max(end, o);
-    }
-    end = max(end, top);
+    int end = ahead;
+    if (e + 32 < p.groups) ahead = offset(e + 33);
+    const int live = min(32, p.groups - e0);
+    if (e >= p.groups) end = 0;
     int begin = __shfl_up_sync(0xFFFFFFFFu, end, 1);
     if (lane == 0) begin = top;
-    int n = 0;
-    if (e < p.groups)
-      n = kRaggedK ? p.tiles_lane * p.tiles_col : (end - begin + p.col_tile - 1) / p.col_tile * p.tiles_lane;
-    #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
-      if (lane >= d) n += o;
+    if (__any_sync(0xFFFFFFFFu, lane < live && end < begin)) {   // an offset falls: the running maximum
+      for (int d = 1; d < live; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, end, d);
+        if (lane >= d) end = max(end, o);
+      }
+      end = max(end, top);
+      begin = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+      if (lane == 0) begin = top;
+    }
+    int n;   // tiles up to and with this group, of this round
+    if constexpr (kRaggedK) {
+      n = (min(lane, live - 1) + 1) * p.tiles_lane * p.tiles_col;
+    } else {
+      n = lane < live ? ((end - begin + p.col_tile - 1) >> p.col_shift) * p.tiles_lane : 0;
+      for (int d = 1; d < live; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, n, d);
+        if (lane >= d) n += o;
+      }
     }
     if (e < p.groups) {
       bound[e + 1] = end;
       first[e + 1] = tiles + n;
     }
-    top = __shfl_sync(0xFFFFFFFFu, end, 31);
-    tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
+    top = __shfl_sync(0xFFFFFFFFu, end, live - 1);
+    tiles += __shfl_sync(0xFFFFFFFFu, n, live - 1);
   }
 }
 
@@ -920,22 +938,19 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
             if (issuer && lane == 0) bulk_wait_read<0>();
             duo_sync(1 + duo);
             if (p.vec_ok) {
-              #pragma unroll
-              for (int it = 0; it < 4; ++it) {
-                const int c = it * 8 + (lane >> 2), q = lane & 3;
-                const int n = n0 + q * 8;
-                const uint4 x = *reinterpret_cast<const uint4*>(buf + c * 128 + (((chunk0 + q) ^ (c & 7)) * 16));
-                if (c < live && n < p.nlane) {
-                  unsigned short* dst = dh + static_cast<int64_t>(c0 + c) * p.ldd + n;
-                  if (n + 8 <= p.nlane) {
-                    *reinterpret_cast<uint4*>(dst) = x;
-                  } else {
-                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-                    #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                      if (n + j < p.nlane) dst[j] = static_cast<unsigned short>(xw[j >> 1] >> (16 * (j & 1)));
-                  }
-                }
+              const int q = lane & 3, n = n0 + q * 8, c1 = lane >> 2;
+              unsigned short* dst = dh + static_cast<int64_t>(c0 + c1) * p.ldd + n;
+              const int64_t pitch = 8 * p.ldd;
+              const uint8_t* from = buf + c1 * 128 + (((chunk0 + q) ^ c1) * 16);   // columns c1, c1 + 8, ...
+              if (n + 8 <= p.nlane) {
+                #pragma unroll
+                for (int it = 0; it < 4; ++it)
+                  if (c1 + 8 * it < live) *reinterpret_cast<uint4*>(dst + it * pitch) = *reinterpret_cast<const uint4*>(from + it * 1024);
+              } else {
+                for (int it = 0; it < 4; ++it)
+                  for (int j = 0; j < 8; ++j)
+                    if (c1 + 8 * it < live && n + j < p.nlane)
+                      dst[it * pitch + j] = *reinterpret_cast<const unsigned short*>(from + it * 1024 + j * 2);
               }
             } else {
               // Rows that 16-byte stores cannot address.  Each of the two

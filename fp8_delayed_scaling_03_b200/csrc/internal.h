@@ -173,7 +173,7 @@ struct GroupedParams {
   int ncol;                   // ragged contraction: output rows of each group
   int tiles_lane, tiles_col;  // tiles_col: ragged contraction only
   int k_blocks;               // 128-byte blocks of the contraction (ragged contraction: of all rows)
-  int col_tile;               // columns per tile: 16, 32, 64, 128 or 256
+  int col_tile, col_shift;    // columns per tile: 16, 32, 64, 128 or 256 = 1 << col_shift
   int split;                  // CTAs of a cluster that share each tile's k-blocks (1: none)
   int stages, smem_bytes;
   int lane_mn;                // the lane operand is MN-major
