@@ -809,13 +809,16 @@ def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch
 @dataclass
 class Int8Result:
     y: torch.Tensor
-    codes: torch.Tensor   # x8 with its rows' padding
     sx: torch.Tensor
+    codes: torch.Tensor   # x8, or the buffer that holds sx and then x8's rows padded to 16
     cols: int
 
     @property
     def x8(self) -> torch.Tensor:
-        return self.codes[:, : self.cols]
+        if self.codes.dtype == torch.int8:
+            return self.codes
+        rows = self.sx.numel()
+        return self.codes[(rows + 3) // 4 * 4:].view(torch.int8).view(rows, (self.cols + 15) // 16 * 16)[:, : self.cols]
 
 
 def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) -> Int8Result:
@@ -839,16 +842,21 @@ def linear_int8(x, w8, sw, bias=None, y=None, x8=None, sx=None, out_dtype=None) 
         y, ldy = x.new_empty(M, N, dtype=out_dtype), N
     else:
         ldy = _matrix(_out(y, (M, N), out_dtype, x, "y"), "y")[2]
-    if x8 is None:
-        ldx8 = (K + 15) // 16 * 16
-        x8 = x.new_empty(M, ldx8, dtype=torch.int8)
+    if x8 is None and sx is None:
+        # one buffer for both: the scales, then the codes' rows
+        ldx8, at = (K + 15) // 16 * 16, (M + 3) // 4 * 4
+        codes = x.new_empty(at + M * ldx8 // 4, dtype=torch.float32)
+        sx = codes.as_strided((M,), (1,))
+        sx_ptr = codes.data_ptr()
+        x8_ptr = sx_ptr + 4 * at
     else:
-        ldx8 = _matrix(_out(x8, (M, K), torch.int8, x, "x8"), "x8")[2]
-    if sx is None:
-        sx = x.new_empty(M, dtype=torch.float32)
-    elif not _out(sx, (M,), torch.float32, x, "sx").is_contiguous():
-        raise ValueError("sx: contiguous")
+        codes = x8 if x8 is not None else x.new_empty(M, (K + 15) // 16 * 16, dtype=torch.int8)[:, :K]
+        ldx8 = _matrix(_out(codes, (M, K), torch.int8, x, "x8"), "x8")[2]
+        sx = _out(sx, (M,), torch.float32, x, "sx")
+        if not sx.is_contiguous():
+            raise ValueError("sx: contiguous")
+        sx_ptr, x8_ptr = sx.data_ptr(), codes.data_ptr()
     _call("fp8_linear_int8_forward", dev, _call_linear_int8,
           _pack_int8(M, N, K, x.data_ptr(), x_dtype, ldx, w8.data_ptr(), ldw, sw.data_ptr(), _address(bias), bias_dtype,
-                     x8.data_ptr(), ldx8, sx.data_ptr(), y.data_ptr(), y_dtype, ldy))
-    return Int8Result(y, x8, sx, K)
+                     x8_ptr, ldx8, sx_ptr, y.data_ptr(), y_dtype, ldy))
+    return Int8Result(y, sx, codes, K)

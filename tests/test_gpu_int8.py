@@ -175,6 +175,11 @@ def test_linear(dtype, M, N, K):
         K * s.cuda().double()[:, None] * sw.double() / 4
     want = x.double() @ w.double().t() + bias.double()
     assert bool(((r.y.double() - want).abs() <= step + want.abs() * torch.finfo(dtype).eps + 1e-5).all())
+    x8, sx = torch.empty(M, (K + 15) // 16 * 16, dtype=torch.int8, device="cuda")[:, :K], torch.empty(M, device="cuda")
+    for given in (dict(x8=x8), dict(sx=sx), dict(x8=x8, sx=sx)):   # the caller's buffers
+        o = F.linear_int8(x, w8, sw, bias=bias, **given)
+        assert torch.equal(o.y, r.y) and torch.equal(o.x8, r.x8) and torch.equal(o.sx, r.sx)
+        assert ("x8" not in given or o.x8 is x8) and ("sx" not in given or o.sx is sx)
     other = F.linear_int8(x, w8, sw, out_dtype=torch.float32)
     assert other.y.dtype == torch.float32
     assert_close(other.y, y, y, torch.float32)
@@ -195,7 +200,9 @@ def test_bad_rows_give_nan_rows_only():
 def test_empty_sizes():
     """No rows, no channels, or an empty contraction, where the bias alone is the result."""
     w8, sw = F.quantize_int8(torch.randn(48, 64).cuda())
-    assert F.linear_int8(torch.empty(0, 64, device="cuda"), w8, sw).y.shape == (0, 48)
+    r = F.linear_int8(torch.empty(0, 64, device="cuda"), w8, sw)
+    assert r.y.shape == (0, 48) and r.x8.shape == (0, 64) and r.sx.shape == (0,)
+    assert F.linear_int8(torch.empty(5, 0, device="cuda"), w8[:, :0], sw).x8.shape == (5, 0)
     assert F.linear_int8(torch.ones(3, 64, device="cuda"), w8[:0], sw[:0]).y.shape == (3, 0)
     bias = torch.randn(48).bfloat16().cuda()
     none = torch.empty(48, 0, dtype=torch.int8, device="cuda")
