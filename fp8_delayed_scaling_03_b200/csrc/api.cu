@@ -916,11 +916,11 @@ int grouped_call(const fp8_mm_args& a, int ragged, const fp8_groups& g, GroupedC
     if (s) return s;
   }
   if (g.groups > 0 && a.m > 0 && a.n > 0 && (!a.d || a.ldd < a.n || !aligned(a.d, 2))) return FP8_ERR_INVALID_ARG;
-  if (!rk && g.groups > 1) {
+  if (!rk && g.groups > 1 && a.n > 0 && a.k > 0) {   // (an empty B has no strides to check)
     if (g.stride_b % 16) return FP8_ERR_MISALIGNED;
     const int64_t outer = a.b_major == FP8_K_MAJOR ? a.n : a.k;
     // stride 0 shares one B; other strides keep the groups' matrices apart
-    if (g.stride_b != 0 && outer > 0 && g.stride_b < outer * a.ldb - a.ldb + (a.b_major == FP8_K_MAJOR ? a.k : a.n))
+    if (g.stride_b != 0 && g.stride_b < outer * a.ldb - a.ldb + (a.b_major == FP8_K_MAJOR ? a.k : a.n))
       return FP8_ERR_INVALID_ARG;
   }
   if (rk && g.groups > 1 && a.m > 0 && g.stride_d < (a.m - 1) * a.ldd + a.n) return FP8_ERR_INVALID_ARG;

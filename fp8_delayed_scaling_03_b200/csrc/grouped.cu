@@ -30,14 +30,35 @@
 //     a warp of its own, as the block lands.
 // The stages of the operand ring take what shared memory the group tables (8
 // bytes a group) leave: 192 KB up to 190 groups, a stage less beyond.
-// Roles as in gemm.cu: warp 0 lane 0 TMA producer, warp 1 MMA issuer, warps
-// 2-9 epilogue over double-buffered TMEM accumulators, every wait bounded.
+// Roles as in gemm.cu: warp 0 TMA producer, warp 1 MMA issuer, warps 2-9
+// epilogue over double-buffered TMEM accumulators, every wait bounded.
 // The epilogue reads 16 lanes x 32 columns per tcgen05.ld.16x256b, whose
 // register layout is the one stmatrix takes: stmatrix.trans turns the block
 // over so that a token's outputs are contiguous in a swizzled slab (64 lanes =
-// 128 bytes, two warps), which leaves by a TMA store.  A block cut by its group's end (which TMA
-// cannot clip: the next group's rows follow) leaves as 16-byte stores guarded
-// by that end, and one of rows that TMA cannot address as single elements.
+// 128 bytes, two warps), which leaves by a TMA store.  A block cut by its
+// group's end (which TMA cannot clip: the next group's rows follow) leaves as
+// 16-byte stores guarded by that end, and one of rows that TMA cannot address
+// as 4-byte stores.
+//
+// Tiles.  Large products run on CTA pairs, 256 lanes x 256 columns: a CTA then
+// loads 32 KB a k-block where a lone one of 128 x 256 loads 48 KB.  Few tokens
+// run on single CTAs with narrow tiles, few tiles on clusters that split K
+// (pick_grouped_tile in api.cu has the rule and its times).
+//
+// Measured on a B200 (graph replay; `of measured`: the copy bandwidth 6.53 TB/s
+// and twice the cuBLAS bf16 burst rate, 3.34 PFLOP/s):
+//   8192 rows in 8 equal groups, 11008 x 4096: forward 257 us (2.88 PFLOP/s,
+//     0.86), dX 241 us (3.06, 0.92), dW 295 us (2.50, 0.75); one group 256, 242
+//     and 242 us.  Short of power these are bound by the loads' latency against
+//     192 KB of stages; run without a pause the card's 1 kW limit holds them at
+//     2.1-2.4 PFLOP/s, where twice cuBLAS bf16's sustained rate is 2.8.
+//     dW's 721 MB of output take 140 us at the 5.1 TB/s that the store path
+//     reaches, and share the memory with the loads.
+//   128 rows over 64 groups, 6912 x 1536: 91 us, 6.1 TB/s of weights (0.92).
+//   4 rows over 8 groups, 4096 x 1024: 5.7 us, of which 3.2 us is what any
+//     launch takes (offsets from L2 and their scan 0.8, first load 1.2, the
+//     store's way out 0.6).
+//   int8, 8192 x 11008 x 4096: 241 us (3.07 PFLOP/s): kind::i8 has fp8's rate.
 #include <algorithm>
 #include <atomic>
 
@@ -236,8 +257,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float load_bias(const void* bias, int dtype, int j) {
-  if (dtype == kFP32) return __ldg(static_cast<const float*>(bias) + j);
-  const unsigned short b = __ldg(static_cast<const unsigned short*>(bias) + j);
+  // (plain loads: the read-only path does not promise to see what the kernel before wrote)
+  if (dtype == kFP32) return static_cast<const float*>(bias)[j];
+  const unsigned short b = static_cast<const unsigned short*>(bias)[j];
   return dtype == kFP16 ? __half2float(__ushort_as_half(b)) : __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
@@ -794,7 +816,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int n = n0 + 8 * j + (lane >> 2);
-          f[j] = n < p.nlane && p.k_blocks > 0 ? __ldg(p.scale_b + n) : 0.0f;
+          f[j] = n < p.nlane && p.k_blocks > 0 ? p.scale_b[n] : 0.0f;
           b[j] = p.bias && n < p.nlane ? load_bias(p.bias, p.bias_dtype, n) : 0.0f;
         }
       } else {
@@ -874,7 +896,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const int c = 8 * i + 2 * (lane & 3) + u;
-              s[u] = c < live && p.k_blocks > 0 ? __ldg(p.scale_a + w.col0 + c0 + c) : 0.0f;
+              s[u] = c < live && p.k_blocks > 0 ? p.scale_a[w.col0 + c0 + c] : 0.0f;
             }
           }
           #pragma unroll

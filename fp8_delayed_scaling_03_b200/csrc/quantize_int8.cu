@@ -44,25 +44,27 @@ __device__ __forceinline__ float value(const Chunk<T>& c, int j) {
 }
 
 // The chunk at column col of a row; elements past the row's end are zero.
+// (Plain loads: the read-only path does not promise to see what the kernel
+// before wrote, and this one starts while that may still run.)
 template <typename T>
 __device__ __forceinline__ Chunk<T> load_chunk(const T* row, int64_t col, int64_t cols, int vec_ok) {
   Chunk<T> c;
   if (vec_ok && col + kChunk <= cols) {
     const uint4* src = reinterpret_cast<const uint4*>(row + col);
     #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) c.w[i] = __ldg(src + i);
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) c.w[i] = src[i];
   } else {
     uint32_t* w = reinterpret_cast<uint32_t*>(c.w);
     if constexpr (sizeof(T) == 4) {
       #pragma unroll
       for (int j = 0; j < kChunk; ++j)
-        w[j] = col + j < cols ? __float_as_uint(__ldg(reinterpret_cast<const float*>(row) + col + j)) : 0u;
+        w[j] = col + j < cols ? __float_as_uint(reinterpret_cast<const float*>(row)[col + j]) : 0u;
     } else {
       #pragma unroll
       for (int j = 0; j < kChunk; j += 2) {
         const unsigned short* h = reinterpret_cast<const unsigned short*>(row) + col + j;
-        w[j >> 1] = (col + j < cols ? static_cast<uint32_t>(__ldg(h)) : 0u) |
-                    (col + j + 1 < cols ? static_cast<uint32_t>(__ldg(h + 1)) << 16 : 0u);
+        w[j >> 1] = (col + j < cols ? static_cast<uint32_t>(h[0]) : 0u) |
+                    (col + j + 1 < cols ? static_cast<uint32_t>(h[1]) << 16 : 0u);
       }
     }
   }

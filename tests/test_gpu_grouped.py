@@ -367,6 +367,17 @@ def test_capture_streams_and_repeats():
     assert F.fp8_get_device_status() == 0
 
 
+def test_empty_contraction():
+    """k = 0: the groups' rows are zero, whatever the scales, the others stay."""
+    off = torch.tensor([1, 3, 3, 40], dtype=torch.int32, device="cuda")
+    nan = torch.full((1,), float("nan"), device="cuda")
+    for n in (32, 33, 5000):
+        y = torch.full((50, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        F.grouped_mm(torch.empty(50, 0, dtype=torch.uint8, device="cuda"),
+                     torch.empty(3, n, 0, dtype=torch.uint8, device="cuda"), off, nan, nan, y=y)
+        assert bool((y[1:40] == 0).all()) and bool((y[:1] == 7).all()) and bool((y[40:] == 7).all())
+
+
 def test_one_weight_for_all_groups():
     """stride_b 0: every group uses the same weight, with scales of their own."""
     c, n, k = [40, 0, 90], 176, 112
