@@ -284,8 +284,9 @@ FP8LIN_API int fp8_mm_batched(const fp8_mm_args* args, int64_t batch, int64_t st
  *     dW_e = G_e^T X_e.  args->k is the number of rows of the A and B buffers,
  *     both MN-major; D_e = d + e * stride_d, zero for an empty group.
  * Sizes are at most 2^31 - 1025.  The other majors, a bias and a forced
- * tile_cfg (FP8_TILE_AUTO only) are FP8_ERR_UNSUPPORTED.  One launch, no workspace, deterministic; a row's
- * result does not depend on the other groups' rows. */
+ * tile_cfg (FP8_TILE_AUTO only) are FP8_ERR_UNSUPPORTED; the workspace is not
+ * used.  One launch, deterministic; a row's result does not depend on the
+ * other groups' rows. */
 #define FP8_MAX_GROUPS 1024
 typedef enum { FP8_RAGGED_M = 0, FP8_RAGGED_K = 1 } fp8_ragged;
 typedef struct fp8_groups {

@@ -185,6 +185,34 @@ def test_linear(dtype, M, N, K):
     assert_close(other.y, y, y, torch.float32)
 
 
+def test_trained_experts_served_in_integers():
+    """The two operators together: an expert layer's forward and backward, a step on its weights by that gradient, then
+    the same experts served in 8-bit integers, group by group, against 64-bit products of the updated weights."""
+    c, N, K = [30, 0, 75, 7], 192, 128
+    rows, E = sum(c), len(c)
+    off = torch.tensor([0, *np.cumsum(c)], dtype=torch.int32, device="cuda")
+    gen = torch.Generator().manual_seed(8)
+    x = torch.randn(rows, K, generator=gen).bfloat16().cuda()
+    w = (torch.randn(E, N, K, generator=gen) / 12).bfloat16().cuda()
+    rings = [F.ScaleRing(4) for _ in range(3)]
+    for _ in range(2):
+        f = F.grouped_linear_forward(x, w, off, rings[0], rings[1])
+        b = F.grouped_linear_backward(f.y, f, off, rings[2])     # the gradient of sum(y^2) / 2
+        w = (w.float() - 0.01 * b.dw.float()).bfloat16()
+    at = 0
+    for e, m in enumerate(c):
+        w8, sw = F.quantize_int8(w[e])
+        r = F.linear_int8(x[at:at + m], w8, sw)
+        xe, we = x[at:at + m].double(), w[e].double()
+        want = xe @ we.t()
+        # each factor is off by at most half a step of its scale, then one rounding to bf16
+        s = r.sx.double()[:, None]
+        off_by = s / 2 * we.abs().sum(1) + xe.abs().sum(1)[:, None] * sw.double() / 2 + K * s * sw.double() / 4
+        assert bool(((r.y.double() - want).abs() <= off_by + (want.abs() + off_by) * 2.0 ** -8 + 1e-6).all()), e
+        at += m
+    assert F.fp8_get_device_status() == 0
+
+
 def test_bad_rows_give_nan_rows_only():
     x = torch.randn(20, 64, generator=torch.Generator().manual_seed(1)).cuda()
     w8, sw = F.quantize_int8(torch.randn(48, 64, generator=torch.Generator().manual_seed(2)).cuda())
