@@ -367,6 +367,55 @@ def test_capture_streams_and_repeats():
     assert F.fp8_get_device_status() == 0
 
 
+def test_calls_in_flight_together():
+    """Two captured graphs and eager calls of other sizes on three streams at once, grouped and int8, with no
+    synchronize between them: each result equals the call's own, run alone, bit for bit."""
+    def operands(seed, rows, n, k, counts):
+        gen = torch.Generator().manual_seed(seed)
+        x8, w8, g8 = codes(rows, k, 0, seed), codes(n, k, 0, seed + 1, batch=len(counts)), codes(rows, n, 1, seed + 2)
+        sx, sw, sg, off = scales(1, seed + 3), scales(len(counts), seed + 4), scales(1, seed + 5), offsets_of(counts)
+        x = torch.randn(rows, k, generator=gen).bfloat16().cuda()
+        q = torch.randint(-127, 128, (n, (k + 15) // 16 * 16), dtype=torch.int8, generator=gen).cuda()[:, :k]
+        qs = torch.rand(n, generator=gen).cuda()
+        outs = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+                for shape in ((rows, n), (rows, k), (len(counts), n, k), (rows, n))]
+
+        def run():
+            F.grouped_mm(x8, w8, off, sx, sw, y=outs[0])
+            F.grouped_linear_backward(g8, F.ForwardResult(None, x8, w8, sx, sw, None, None), off, None, g_scale_in=sg,
+                                      dx=outs[1], dw=outs[2])
+            F.linear_int8(x, q, qs, y=outs[3])
+        return outs, run
+
+    sets = [operands(1, 40, 272, 1040, [7, 0, 33]), operands(20, 900, 520, 384, [300, 1, 599]),
+            operands(40, 3, 1511, 1000, [1, 1, 1])]
+    want = []
+    for outs, run in sets:
+        run()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+    graphs = []
+    for _, run in sets[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run()
+    for outs, _ in sets:
+        for o in outs:
+            o.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(30):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+        with torch.cuda.stream(streams[2]):
+            sets[2][1]()
+    torch.cuda.synchronize()
+    for (outs, _), ref in zip(sets, want):
+        assert all(torch.equal(o, r) for o, r in zip(outs, ref))
+    assert F.fp8_get_device_status() == 0
+
+
 def test_empty_contraction():
     """k = 0: the groups' rows are zero, whatever the scales, the others stay."""
     off = torch.tensor([1, 3, 3, 40], dtype=torch.int32, device="cuda")
