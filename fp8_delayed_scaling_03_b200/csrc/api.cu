@@ -737,12 +737,11 @@ int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile, int64_t tile_l
   return tl * (c.rows / col_tile + std::min(c.groups, c.rows));
 }
 
-// Tiles of a launch.  A ragged contraction takes CTA pairs (256 x 256) where
-// they fill the pairs of SMs, else 128 x 128 on one CTA.  Products of tokens
-// take the cheapest of
-//   one CTA, 128 lanes x t columns, t = 16 .. 256;
+// Tiles of a launch: the cheapest of
+//   one CTA, 128 lanes x t columns, t = 16 .. 256 (a ragged contraction: 128
+//   or 256);
 //   the same with its k-blocks split over a cluster of 2 .. 4 CTAs (few tiles
-//   and a long contraction);
+//   of tokens and a long contraction);
 //   a CTA pair, 256 lanes x 256 columns,
 // by the time of the most loaded CTA, whose tiles' main loops and outputs
 // overlap: main + output + (waves - 1) max(main + 0.25, output).  The times, in
@@ -753,6 +752,13 @@ int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile, int64_t tile_l
 //   as on a pair; an output 1.0 + 0.3 for each two 32-column steps (0.95 where
 //   D's rows cannot take 16-byte stores); joining s partial sums
 //   0.9 + (s - 1) (0.4 + 0.5 (t / 64)^2).
+// A ragged contraction's tiles (84 shapes of 1 to 8192 rows, 1 to 64 groups, D
+// of 64 to 11008 rows and columns, all three timed: within 2 % of the best for
+// each; of 63 more, drawn, within 3 % for 62, 7 % at most): as above, 256 columns on one CTA a block 0.39 and 0.01 more an output
+// for each block, as they load more than the pair's; a pair 0.3 once, for its
+// cluster.  At 22 groups, 1 row, D 10181 x 128: one CTA with 256 columns 14.6,
+// with 128 18.6, a pair (half its lanes past D) 25.3 us.  At 16 groups, 4096
+// rows, D 6912 x 1536: 77.5, 90.7 and 74.0 us.
 // Group sizes are not known here: a group is taken to need half a tile more
 // than its average rows fill, one at least.  Where the weights' bytes bound
 // the time the choices hardly differ, and the smallest tile, which loads the
@@ -761,22 +767,28 @@ void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair, int
   const int64_t tl = (c.nlane + 127) / 128, tl2 = (c.nlane + 255) / 256;
   *split = 1;
   *tile = 256;
-  if (c.ragged_k) {
-    *pair = tl2 * ((c.ncol + 255) / 256) * c.groups >= sms / 2;
-    if (!*pair) *tile = 128;
-    return;
-  }
   const double live = static_cast<double>(std::max<int64_t>(1, std::min(c.groups, c.rows)));
   const double avg = static_cast<double>(c.rows) / live;
   const int64_t kb = (c.k + 127) / 128;
-  const bool wide = aligned(c.d, 16) && (c.ldd * esize(c.d_dtype)) % 16 == 0;
+  const bool wide = aligned(c.d, 16) && (c.ldd * esize(c.d_dtype)) % 16 == 0 && (!c.ragged_k || c.stride_d * 2 % 16 == 0);
   auto col_tiles = [&](double t) { return c.groups == 1 ? std::ceil(avg / t) : live * std::max(1.0, avg / t + 0.5); };
-  auto time = [&](double units, int slots, int64_t blocks, double t_kb, int64_t t) {
+  auto time = [&](double units, int slots, int64_t blocks, double t_kb, int64_t t, double more = 0.0) {
     const double main = t_kb * static_cast<double>(blocks);
-    const double out = 1.0 + static_cast<double>((t + 63) / 64) * (wide ? 0.3 : 0.95);
+    const double out = 1.0 + static_cast<double>((t + 63) / 64) * (wide ? 0.3 : 0.95) + more;
     return main + out + (std::ceil(units / std::max(1, slots)) - 1.0) * std::max(main + 0.25, out);
   };
   *pair = true;
+  if (c.ragged_k) {
+    const int64_t blocks = static_cast<int64_t>(std::ceil(avg / 128.0));
+    const double lanes = static_cast<double>(tl * c.groups);
+    const double on_pair = 0.3 + time(static_cast<double>(tl2 * c.groups * ((c.ncol + 255) / 256)), sms / 2, blocks, 0.36, 256);
+    const double wide_one = time(lanes * static_cast<double>((c.ncol + 255) / 256), sms, blocks, 0.39, 256,
+                                 0.01 * static_cast<double>(blocks));
+    const double one = time(lanes * static_cast<double>((c.ncol + 127) / 128), sms, blocks, 0.25, 128);
+    *pair = on_pair < std::min(one, wide_one);
+    if (!*pair && one < wide_one) *tile = 128;
+    return;
+  }
   double best = time(col_tiles(256) * static_cast<double>(tl2), sms / 2, kb, 0.36, 256);
   for (int64_t t = 16; t <= 256; t *= 2) {
     const double t_kb = t <= 32 ? 0.17 : (t == 64 ? 0.21 : (t == 128 ? 0.25 : 0.36));

@@ -42,7 +42,8 @@
 //
 // Tiles.  Large products run on CTA pairs, 256 lanes x 256 columns: a CTA then
 // loads 32 KB a k-block where a lone one of 128 x 256 loads 48 KB.  Few tokens
-// run on single CTAs with narrow tiles, few tiles on clusters that split K
+// run on single CTAs with narrow tiles, few tiles on clusters that split K, and
+// dW of few rows a group, which its output bounds, on single CTAs
 // (pick_grouped_tile in api.cu has the rule and its times).
 //
 // Measured on a B200 (graph replay; `of measured`: the copy bandwidth 6.53 TB/s

@@ -133,6 +133,26 @@ def test_large_products(c, n, k):
     assert F.fp8_get_device_status() == 0
 
 
+@pytest.mark.parametrize("n,k", [(300, 100), (1300, 84), (2049, 128), (260, 1000), (128, 1100)])
+def test_weight_gradient_of_many_groups(n, k):
+    """More tiles than SMs, most of few columns or rows: 256 columns on one CTA, the last tiles narrower than one chunk
+    of 128; groups without rows have a zero gradient; NaN codes of the neighbours stay out."""
+    c = [0, 90, 1, 33, 128, 0, 97, 257, 160, 5] * 5
+    rows = sum(c) + 4
+    x8, g8, off = codes(rows, k, 0, 5), codes(rows, n, 1, 6), offsets_of(c, 2)
+    x8[:2], x8[rows - 2:], g8[:2], g8[rows - 2:] = 0x7F, 0x7F, 0x7F, 0x7F
+    fwd = F.ForwardResult(None, x8, codes(n, k, 0, 7, batch=len(c)), scales(1, 8), scales(1, 9), None, None)
+    sg = scales(1, 10)
+    b = F.grouped_linear_backward(g8, fwd, off, None, need_dx=False, g_scale_in=sg)
+    at = 2
+    for e, m in enumerate(c):
+        x, g = value(x8[at:at + m], 0), value(g8[at:at + m], 1)
+        s = float(sg) * float(fwd.sx)
+        assert_close(b.dw[e], g.t() @ x / s, g.abs().t() @ x.abs() / s, (e, m))
+        at += m
+    assert F.fp8_get_device_status() == 0
+
+
 @pytest.mark.parametrize("c", [[1], [1, 0, 2, 0, 0, 1, 0, 3], [40, 0, 20], [64], [33], [0, 0, 5]])
 @pytest.mark.parametrize("n,k", [(130, 1024), (400, 1100), (24, 8192), (1000, 2050)])
 @pytest.mark.parametrize("major", ["K", "MN"])
