@@ -985,39 +985,47 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
               unsigned short* const dst = dh + static_cast<int64_t>(c0 + (qd & 1)) * p.ldd + nd;
               const int64_t pitch = 2 * p.ldd;
               const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
-              auto at = [&](int c, int j) {
-                return buf + c * 128 + (((j >> 3) ^ (c & 7)) * 16) + (j & 7) * 2;
-              };
-              const int j = 2 * lane + shift;
-              const int j1 = min(j + 1, 63);
-              const bool pair = j + 1 < min(left, 64), single = !pair && j < left;   // (single: an odd row's or D's last lane)
+              const int row0 = qd & 1, rows = (live + 1 - row0) >> 1;   // this warp's columns: row0, row0 + 2, ...
+              const int end = min(left, 64);
+              auto at = [&](int c, int j) { return c * 128 + (((j >> 3) ^ (c & 7)) * 16) + (j & 7) * 2; };
+              const int j = 2 * lane + shift, j1 = min(j + 1, 63);
+              const bool pair = j + 1 < end;
+              // the swizzle repeats every eight columns, this warp's four
+              int off[4], off1[4];
+              #pragma unroll
+              for (int i = 0; i < 4; ++i) off[i] = at(2 * i + row0, j), off1[i] = at(2 * i + row0, j1);
               #pragma unroll 1
-              for (int i0 = 0; i0 < 16; i0 += 8) {
+              for (int i0 = 0; i0 < rows; i0 += 8) {
                 // eight rows' pairs, then their stores: no store waits for a
                 // load (one row at a time took twice as long)
+                const uint8_t* const from = buf + i0 * 256;
                 uint32_t x[8];
                 if (shift) {
                   #pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const int c = 2 * (i0 + i) + (qd & 1);
-                    x[i] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(at(c, j))) |
-                           static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(at(c, j1))) << 16;
+                  for (int i = 0; i < 8; ++i)
+                    x[i] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(from + off[i & 3] + (i >> 2) * 1024)) |
+                           static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(from + off1[i & 3] + (i >> 2) * 1024)) << 16;
+                } else {
+                  #pragma unroll
+                  for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(from + off[i & 3] + (i >> 2) * 1024);
+                }
+                unsigned short* to = dst + i0 * pitch + j;
+                if (i0 + 8 <= rows) {
+                  if (pair) {
+                    #pragma unroll
+                    for (int i = 0; i < 8; ++i, to += pitch) *reinterpret_cast<uint32_t*>(to) = x[i];
                   }
                 } else {
                   #pragma unroll
-                  for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(at(2 * (i0 + i) + (qd & 1), j));
-                }
-                unsigned short* to = dst + i0 * pitch + j;
-                #pragma unroll
-                for (int i = 0; i < 8; ++i, to += pitch) {
-                  if (2 * (i0 + i) + (qd & 1) < live) {
-                    if (pair) *reinterpret_cast<uint32_t*>(to) = x[i];
-                    if (single) *to = static_cast<unsigned short>(x[i]);
-                  }
+                  for (int i = 0; i < 8; ++i, to += pitch)
+                    if (pair && i0 + i < rows) *reinterpret_cast<uint32_t*>(to) = x[i];
                 }
               }
-              if (shift && lane < 16 && 2 * lane + (qd & 1) < live && left > 0)
-                dst[lane * pitch] = *reinterpret_cast<const unsigned short*>(at(2 * lane + (qd & 1), 0));
+              // the odd ends, a lane each: rows' first elements by lanes 0-15, their last ones by lanes 16-31
+              const int je = lane < 16 ? 0 : end - 1, row = lane & 15;
+              const bool odd = lane < 16 ? shift != 0 : ((end - shift) & 1) != 0;
+              if (odd && row < rows && end > (lane < 16 ? 0 : shift))
+                dst[row * pitch + je] = *reinterpret_cast<const unsigned short*>(buf + at(2 * row + row0, je));
             }
             __syncwarp();
           }
