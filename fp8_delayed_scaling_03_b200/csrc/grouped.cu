@@ -994,34 +994,31 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
               int off[4], off1[4];
               #pragma unroll
               for (int i = 0; i < 4; ++i) off[i] = at(2 * i + row0, j), off1[i] = at(2 * i + row0, j1);
-              #pragma unroll 1
-              for (int i0 = 0; i0 < rows; i0 += 8) {
-                // eight rows' pairs, then their stores: no store waits for a
-                // load (one row at a time took twice as long)
-                const uint8_t* const from = buf + i0 * 256;
-                uint32_t x[8];
-                if (shift) {
-                  #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    x[i] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(from + off[i & 3] + (i >> 2) * 1024)) |
-                           static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(from + off1[i & 3] + (i >> 2) * 1024)) << 16;
-                } else {
-                  #pragma unroll
-                  for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint32_t*>(from + off[i & 3] + (i >> 2) * 1024);
-                }
-                unsigned short* to = dst + i0 * pitch + j;
-                if (i0 + 8 <= rows) {
-                  if (pair) {
-                    #pragma unroll
-                    for (int i = 0; i < 8; ++i, to += pitch) *reinterpret_cast<uint32_t*>(to) = x[i];
-                  }
-                } else {
-                  #pragma unroll
-                  for (int i = 0; i < 8; ++i, to += pitch)
-                    if (pair && i0 + i < rows) *reinterpret_cast<uint32_t*>(to) = x[i];
-                }
+              // all rows' pairs, then their stores: no store waits for a load
+              // (eight rows at a time took 1.15 times as long, one 3 times)
+              uint32_t x[16];
+              if (shift) {
+                #pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  x[i] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(buf + off[i & 3] + (i >> 2) * 1024)) |
+                         static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(buf + off1[i & 3] + (i >> 2) * 1024)) << 16;
+              } else {
+                #pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = *reinterpret_cast<const uint32_t*>(buf + off[i & 3] + (i >> 2) * 1024);
               }
-              // the odd ends, a lane each: rows' first elements by lanes 0-15, their last ones by lanes 16-31
+              unsigned short* to = dst + j;
+              if (rows == 16) {
+                if (pair) {
+                  #pragma unroll
+                  for (int i = 0; i < 16; ++i, to += pitch) *reinterpret_cast<uint32_t*>(to) = x[i];
+                }
+              } else {
+                #pragma unroll
+                for (int i = 0; i < 16; ++i, to += pitch)
+                  if (pair && i < rows) *reinterpret_cast<uint32_t*>(to) = x[i];
+              }
+              // the odd ends, a lane each: rows' first elements by lanes 0-15, their
+              // last ones by lanes 16-31 (loaded before the stores they cost more than that hid)
               const int je = lane < 16 ? 0 : end - 1, row = lane & 15;
               const bool odd = lane < 16 ? shift != 0 : ((end - shift) & 1) != 0;
               if (odd && row < rows && end > (lane < 16 ? 0 : shift))
