@@ -749,16 +749,18 @@ int64_t grouped_max_tiles(const GroupedCall& c, int64_t col_tile, int64_t tile_l
 // groups, every choice timed; the rule's is within 3 % of the best for 19 of
 // them, 14 % at most):
 //   a k-block of up to 32 columns 0.17, 64 0.21, 128 0.25, 256 0.36 on one CTA
-//   as on a pair; an output 1.0 + 0.3 for each two 32-column steps (0.95 where
-//   D's rows cannot take 16-byte stores); joining s partial sums
-//   0.9 + (s - 1) (0.4 + 0.5 (t / 64)^2).
-// A ragged contraction's tiles (84 shapes of 1 to 8192 rows, 1 to 64 groups, D
-// of 64 to 11008 rows and columns, all three timed: within 2 % of the best for
-// each; of 63 more, drawn, within 3 % for 62, 7 % at most): as above, 256 columns on one CTA a block 0.39 and 0.01 more an output
-// for each block, as they load more than the pair's; a pair 0.3 once, for its
-// cluster.  At 22 groups, 1 row, D 10181 x 128: one CTA with 256 columns 14.6,
-// with 128 18.6, a pair (half its lanes past D) 25.3 us.  At 16 groups, 4096
-// rows, D 6912 x 1536: 77.5, 90.7 and 74.0 us.
+//   as on a pair; an output 1.0 + 0.3 for each two 32-column steps (0.6 where
+//   D's rows cannot take 16-byte stores: of 40 drawn such shapes the choice is
+//   within 3 % for 33, 12 % at most);
+//   joining s partial sums 0.9 + (s - 1) (0.4 + 0.5 (t / 64)^2).
+// A ragged contraction's tiles (192 shapes of 1 to 8192 rows, 1 to 64 groups, D
+// of 64 to 11008 rows and columns, all three timed: within 3 % of the best for
+// 185, 8 % at most, repeated timings' own differences included): as above, 256
+// columns on one CTA a block 0.39 and 0.01 more an output for each block, as
+// they load more than the pair's; a pair 0.3 once, for its cluster.  At 22
+// groups, 1 row, D 10181 x 128: one CTA with 256 columns 14.8, with 128 18.5, a
+// pair (half its lanes past D) 25.5 us.  At 16 groups, 4096 rows, D 6912 x
+// 1536: 76.4, 88.7 and 72.9 us.
 // Group sizes are not known here: a group is taken to need half a tile more
 // than its average rows fill, one at least.  Where the weights' bytes bound
 // the time the choices hardly differ, and the smallest tile, which loads the
@@ -774,7 +776,7 @@ void pick_grouped_tile(const GroupedCall& c, int sms, int* tile, bool* pair, int
   auto col_tiles = [&](double t) { return c.groups == 1 ? std::ceil(avg / t) : live * std::max(1.0, avg / t + 0.5); };
   auto time = [&](double units, int slots, int64_t blocks, double t_kb, int64_t t, double more = 0.0) {
     const double main = t_kb * static_cast<double>(blocks);
-    const double out = 1.0 + static_cast<double>((t + 63) / 64) * (wide ? 0.3 : 0.95) + more;
+    const double out = 1.0 + static_cast<double>((t + 63) / 64) * (wide ? 0.3 : 0.6) + more;
     return main + out + (std::ceil(units / std::max(1, slots)) - 1.0) * std::max(main + 0.25, out);
   };
   *pair = true;
