@@ -643,6 +643,16 @@ def _codes_fmt(t: torch.Tensor, fmt: int, what: str) -> None:
         raise ValueError(f"{what}: expected fp8 codes of format {fmt}, got {t.dtype}")
 
 
+def _own_codes(t: torch.Tensor, given: torch.Tensor | None, what: str) -> torch.Tensor:
+    """The uint8 view of an operand that comes as fp8 codes.  The kernels read it in place: a caller's buffer for its
+    codes would stay unwritten, so none but the operand itself is taken."""
+    codes = t if t.dtype is torch.uint8 else t.view(torch.uint8)
+    if given is not None and given is not t and (given.data_ptr() != codes.data_ptr() or given.shape != codes.shape or
+                                                 given.stride() != codes.stride() or given.element_size() != 1):
+        raise ValueError(f"{what}: the operand is already fp8 codes and used in place, a buffer for them would stay unwritten")
+    return codes
+
+
 def _operand_dtype(t: torch.Tensor, fmt: int) -> tuple[int, bool]:
     """(FP8_DT_*, whether it holds fp8 codes) of a linear's operand."""
     if t.dtype in _CODE_TYPES:
@@ -705,7 +715,8 @@ def grouped_linear_forward(x, w, offsets, ring_x: ScaleRing | None, ring_w: Scal
                            w8=None) -> ForwardResult:
     """y = x w[e]^T for the rows of each group e, through fp8_linear_grouped_forward: the linear_forward of a mixture
     of experts.  x [rows, K] sorted by expert, w [groups, N, K]; either may be bf16/fp16/fp32 or fp8 codes with its
-    *_scale_in (w's: one scale, or one per group).  w8 is [groups, N, K]."""
+    *_scale_in (w's: one scale, or one per group).  x8 and w8 [groups, N, K] are buffers for the codes of a wide
+    operand; one that is codes already is used in place and takes none."""
     groups, off64 = _offsets(offsets)
     M, K, ldx = _matrix(x, "x")
     N, kw, ldw = _experts(w, groups, "w")
@@ -714,15 +725,19 @@ def grouped_linear_forward(x, w, offsets, ring_x: ScaleRing | None, ring_w: Scal
     (xd, xq), (wd, wq) = _operand_dtype(x, fmt_x), _operand_dtype(w, fmt_w)
     step = _scale_step(w_scale_in, groups, "w_scale_in") if wq and w_scale_in is not None else 0
     ring_x_buf, ring_w_buf = ring_x and ring_x.buf, ring_w and ring_w.buf
+    if xq:
+        x8 = _own_codes(x, x8, "x8")
+    if wq:
+        w8 = _own_codes(w, w8, "w8")
     dev = _one_device(x, w, offsets, x_scale_in, w_scale_in, x8, w8, y, ring_x_buf, ring_w_buf)
     if ring_x is not None and ring_w is not None and ring_x.H != ring_w.H:
         raise ValueError("ring_x and ring_w of one history length")
     H = ring_x.H if ring_x is not None else (ring_w.H if ring_w is not None else hist_len)
     y = _out(y, (M, N), torch.bfloat16, x, "y")
     if x8 is None:
-        x8 = x.view(torch.uint8) if xq else fp8_alloc(M, K, x.device)
+        x8 = fp8_alloc(M, K, x.device)
     if w8 is None:
-        w8 = w.view(torch.uint8) if wq else fp8_alloc_experts(groups, N, K, x.device)
+        w8 = fp8_alloc_experts(groups, N, K, x.device)
     if tuple(x8.shape) != (M, K) or tuple(w8.shape) != (groups, N, K) or x8.dtype != torch.uint8 or \
             w8.dtype != torch.uint8:
         raise ValueError("x8 [rows, K] and w8 [groups, N, K] as uint8 codes")
@@ -742,7 +757,7 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
                             g8=None) -> BackwardResult:
     """dx [rows, K] and dw [groups, N, K] through fp8_linear_grouped_backward, reusing the forward's x8, w8 and scale
     snapshots.  Rows of dx outside every group are left as they were (or not initialized).  For a g that comes as fp8
-    codes the result's sg is g_scale_in and its amax_g None."""
+    codes the result's g8 is g itself (another g8 buffer is refused), its sg g_scale_in and its amax_g None."""
     groups, off64 = _offsets(offsets)
     M, N, ldg = _matrix(g, "g")
     x8, w8, sx, sw = fwd.x8, fwd.w8, fwd.sx, fwd.sw
@@ -757,10 +772,10 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
     step = _scale_step(sw, groups, "sw")
     gd, gq = _operand_dtype(g, fmt_g)
     ring_buf = ring_g and ring_g.buf
+    if gq:
+        g8, ldg8 = _own_codes(g, g8, "g8"), ldg
     dev = _one_device(g, x8, w8, offsets, sx, sw, g_scale_in, dx, dw, g8, ring_buf)
-    if gq and (g8 is None or g8 is g):
-        g8, ldg8 = (g if g.dtype == torch.uint8 else g.view(torch.uint8)), ldg
-    else:
+    if not gq:
         g8 = fp8_alloc(M, N, g.device) if g8 is None else g8
         ldg8 = _matrix(_out(g8, (M, N), torch.uint8, g, "g8"), "g8")[2]
     lddx = lddw = K
