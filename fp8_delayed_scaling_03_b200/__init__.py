@@ -627,6 +627,11 @@ def _offsets(t: torch.Tensor) -> tuple[int, int]:
     return shape[0] - 1, int(dtype == torch.int64)
 
 
+def _one_scale(scale: torch.Tensor, what: str) -> None:
+    if scale.numel() != 1 or scale.dtype is not _FP32:
+        raise ValueError(f"{what}: one fp32 scale, got {scale.dtype} {tuple(scale.shape)}")
+
+
 def _scale_step(scale: torch.Tensor, groups: int, what: str) -> int:
     n = scale.numel()
     if scale.dtype is not _FP32 or (n != 1 and n != groups) or not scale.is_contiguous():
@@ -695,8 +700,7 @@ def grouped_mm(x8, w8, offsets, sx, sw, y=None, fmt_x=FP8_E4M3, fmt_w=FP8_E4M3, 
         raise ValueError(f"x8 and w8 of one contraction length: {tuple(x8.shape)}, {tuple(w8.shape)}")
     _codes_fmt(x8, fmt_x, "x8")
     _codes_fmt(w8, fmt_w, "w8")
-    if sx.numel() != 1 or sx.dtype is not _FP32:
-        raise ValueError("sx: one fp32 scale")
+    _one_scale(sx, "sx")
     step = _scale_step(sw, groups, "sw")
     dev = _one_device(x8, w8, offsets, sx, sw, y)
     if y is None:
@@ -727,6 +731,8 @@ def grouped_linear_forward(x, w, offsets, ring_x: ScaleRing | None, ring_w: Scal
     ring_x_buf, ring_w_buf = ring_x and ring_x.buf, ring_w and ring_w.buf
     if xq:
         x8 = _own_codes(x, x8, "x8")
+        if x_scale_in is not None:
+            _one_scale(x_scale_in, "x_scale_in")
     if wq:
         w8 = _own_codes(w, w8, "w8")
     dev = _one_device(x, w, offsets, x_scale_in, w_scale_in, x8, w8, y, ring_x_buf, ring_w_buf)
@@ -767,13 +773,14 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
         raise ValueError(f"g {tuple(g.shape)}, x8 {tuple(x8.shape)} and w8 {tuple(w8.shape)} do not fit")
     _codes_fmt(x8, fmt_x, "x8")
     _codes_fmt(w8, fmt_w, "w8")
-    if sx.numel() != 1 or sx.dtype is not _FP32:
-        raise ValueError("sx: one fp32 scale")
+    _one_scale(sx, "sx")
     step = _scale_step(sw, groups, "sw")
     gd, gq = _operand_dtype(g, fmt_g)
     ring_buf = ring_g and ring_g.buf
     if gq:
         g8, ldg8 = _own_codes(g, g8, "g8"), ldg
+        if g_scale_in is not None:
+            _one_scale(g_scale_in, "g_scale_in")
     dev = _one_device(g, x8, w8, offsets, sx, sw, g_scale_in, dx, dw, g8, ring_buf)
     if not gq:
         g8 = fp8_alloc(M, N, g.device) if g8 is None else g8

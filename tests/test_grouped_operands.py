@@ -63,3 +63,24 @@ def test_buffers_of_operands_quantized_here(fp8):
         forward(fp8, o, x=x, w=w, x8=o["x"], w8=o["w"])
     with pytest.raises(ValueError, match=NOT_ON_GPU):
         backward(fp8, o, g=g, g8=o["g"])
+
+
+def test_scales_of_codes_are_one_fp32_value(fp8):
+    """The kernels read a scale as one fp32 word: another type would be read as another number, an empty tensor past
+    its end."""
+    o = operands()
+    bad = (torch.ones(1, dtype=torch.float64), torch.ones(1, dtype=torch.bfloat16), torch.ones(2), torch.ones(0),
+           torch.ones(1, dtype=torch.int32))
+    for s in bad:
+        with pytest.raises(ValueError, match="x_scale_in"):
+            forward(fp8, o, x_scale_in=s)
+        with pytest.raises(ValueError, match="g_scale_in"):
+            backward(fp8, o, g_scale_in=s)
+    for s in (torch.ones(()), torch.ones(1, 1), torch.ones(4)[2:3]):
+        with pytest.raises(ValueError, match=NOT_ON_GPU):
+            forward(fp8, o, x_scale_in=s)
+        with pytest.raises(ValueError, match=NOT_ON_GPU):
+            backward(fp8, o, g_scale_in=s)
+    # a wide operand's scale comes from its ring or its amax: what is passed is not read
+    with pytest.raises(ValueError, match=NOT_ON_GPU):
+        forward(fp8, o, x=torch.zeros(4, 16), x_scale_in=bad[0])
