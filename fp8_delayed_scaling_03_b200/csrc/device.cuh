@@ -110,6 +110,62 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* s
   }
 }
 
+// mbar_wait whose probes let the hardware suspend the warp for up
+// to a millisecond until the phase completes.  Without the hint a waiting warp
+// probes again and again; eight epilogue warps doing so through a mainloop
+// cost issue slots and, at the power limit, clock.
+__device__ __forceinline__ bool mbar_await(uint64_t* bar, uint32_t parity, int* status, volatile int* abort,
+                                           uint64_t limit_ns = FP8LIN_WAIT_LIMIT_NS) {
+  const uint32_t a = smem_u32(bar);
+  auto probe = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+  };
+  if (probe()) return true;
+  const uint64_t t0 = globaltimer_ns();
+  #pragma unroll 1
+  while (true) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (probe()) return true;
+    if (abort && *abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      if (status) atomicExch(status, kDevTimeout);
+      if (abort) *abort = 1;
+      return false;
+    }
+  }
+}
+
+// Barriers of two warps (64 threads), the second with a vote.
+__device__ __forceinline__ void duo_sync(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool duo_all(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// mbar_await by two warps that barriers of 64 threads join: true for all of
+// their threads or for none, so that neither is left at such a barrier alone.
+__device__ __forceinline__ bool duo_await(int id, uint64_t* bar, uint32_t parity, int* status, volatile int* abort,
+                                          uint64_t limit_ns = FP8LIN_WAIT_LIMIT_NS) {
+  return duo_all(id, mbar_await(bar, parity, status, abort, limit_ns));
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {

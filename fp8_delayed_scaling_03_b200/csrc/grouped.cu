@@ -122,39 +122,6 @@ __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// mbar_wait (device.cuh) whose probes let the hardware suspend the warp for up
-// to a millisecond until the phase completes.  Without the hint a waiting warp
-// probes again and again; eight epilogue warps doing so through a mainloop
-// cost issue slots and, at the power limit, clock.
-__device__ __forceinline__ bool mbar_await(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
-  const uint32_t a = smem_u32(bar);
-  auto probe = [&]() {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(a), "r"(parity), "r"(1000000u)
-        : "memory");
-    return ok != 0;
-  };
-  if (probe()) return true;
-  const uint64_t t0 = globaltimer_ns();
-  #pragma unroll 1
-  while (true) {
-    #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (probe()) return true;
-    if (abort && *abort) return false;
-    if (globaltimer_ns() - t0 > FP8LIN_WAIT_LIMIT_NS) {
-      if (status) atomicExch(status, kDevTimeout);
-      if (abort) *abort = 1;
-      return false;
-    }
-  }
-}
-
 // Whether a phase has completed, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -166,21 +133,6 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
-}
-
-// Barriers of two epilogue warps (64 threads), the second with a vote.
-__device__ __forceinline__ void duo_sync(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool duo_all(int id, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.red.and.pred q, %2, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "r"(id)
-      : "memory");
-  return r != 0;
 }
 
 // One lane of a converged warp, always the same.
@@ -808,7 +760,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         else mbar_arrive(&tempty[a]);
       }
     };
-    for (Tiles at(p, unit, units); at.t < tiles && !*abort_flag; at.advance(p)) {
+    for (Tiles at(p, unit, units); at.t < tiles; at.advance(p)) {
       const Tile w = tile_at(at);
       const int n0 = w.lane0 + rank * kLanes + qd * 32;       // first output column of this warp
       const int steps = (w.cols + 31) / 32;
@@ -829,15 +781,16 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
         }
         f[0] = (kRaggedK ? w.kb : p.k_blocks) > 0 ? held_f : 0.0f;
       }
-      // two warps leave together: a lane that gave up must not strand the
-      // others at the next barrier
-      if (!duo_all(1 + duo, mbar_await(&tfull[acc], acc_phase, p.status, abort_flag))) break;
+      // The two warps of a slab leave together, here or below: one that gave up
+      // alone, for a wait of its own or for the abort flag, would strand the
+      // other at their next barrier.
+      if (!duo_await(1 + duo, &tfull[acc], acc_phase, p.status, abort_flag)) break;
       tc_fence_after();
       if constexpr (kSplit) {
         if (part == 0) {
           if (ew == 0 && lane == 0)
             mbar_arrive_expect_tx(joined, static_cast<uint32_t>((p.split - 1) * steps * 32 * kLanes * 4));
-          if (!duo_all(1 + duo, mbar_await(joined, 0, p.status, abort_flag))) break;
+          if (!duo_await(1 + duo, joined, 0, p.status, abort_flag)) break;
         }
       }
       uint8_t* const d = static_cast<uint8_t*>(p.d) +

@@ -517,8 +517,10 @@ FP8LIN_API int fp8_get_device_status(void);
  * step of the path): one tiny kernel waits, with a time limit of limit_ns
  * nanoseconds (1 ns .. 2 s), on the 32-bit device word *flag becoming
  * non-zero (the stream-K flag protocol) and on an mbarrier that nothing ever
- * arrives on (the GEMM pipeline protocol).  results (device, 2 ints): 1 where
- * the wait was satisfied, 0 where it ran out.  A wait that runs out records
+ * arrives on (the GEMM pipeline protocol; a second one by two warps that have
+ * to give up together, as the grouped product's epilogue does).  results
+ * (device, 2 ints): 1 where the wait was satisfied, 0 where it ran out, -1 in
+ * the second where the two warps did not agree.  A wait that runs out records
  * FP8_ERR_DEVICE_TIMEOUT for fp8_get_device_status; the kernel then returns,
  * and the context stays usable.  flag and results 4-byte aligned, else
  * FP8_ERR_INVALID_ARG. */
