@@ -166,6 +166,18 @@ __device__ __forceinline__ bool duo_await(int id, uint64_t* bar, uint32_t parity
   return duo_all(id, mbar_await(bar, parity, status, abort, limit_ns));
 }
 
+// Called by one thread behind a block's last barrier.  If a wait of the block
+// gave up, copies it started (or another block of its cluster started for it)
+// may still be on their way to its shared memory: they take microseconds, and
+// get kSettleNs, before the memory is another block's.  A block that did not
+// give up has seen all of its copies land.
+constexpr uint64_t kSettleNs = 10000000;
+__device__ __forceinline__ void settle_copies(const volatile int* abort) {
+  if (!*abort) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < kSettleNs) __nanosleep(1000);
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {

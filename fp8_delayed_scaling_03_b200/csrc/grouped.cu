@@ -174,6 +174,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// A word in the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
 // 16 bytes into the shared memory of a CTA of the cluster; their arrival is
 // counted on its mbarrier.
 __device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar) {
@@ -695,6 +700,9 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
       __syncwarp();
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
+    // Given up: the other CTA's loads were waited for here alone, so it has to
+    // know (settle_copies).
+    if (kPair && !ok && elect_one()) st_cluster_u32(mapa_shared(smem_u32(const_cast<const int*>(abort_flag)), 1), 1u);
     // no MMA may still read shared memory or TMEM when the CTAs tear down
     if (issued && elect_one()) {
       if constexpr (kPair) umma_commit_pair(smem_u32(drain));
@@ -995,6 +1003,7 @@ __global__ void __launch_bounds__(kRaggedK ? kThreadsRaggedK : kThreads, 1)
   tc_fence_before();
   if constexpr (kPair || kSplit) cluster_sync();  // no CTA leaves while another still signals or writes it
   else cta_sync();
+  if (threadIdx.x == 0) settle_copies(abort_flag);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(128) wait_selftest_kernel(const uint32_t* flag
   }
   __syncthreads();
   if (threadIdx.x == 32) results[1] = left[0] == left[1] && left[0] == kDuoTiles - 1 ? alone : -1;
+  if (threadIdx.x == 0) settle_copies(&gave_up);   // (no copies here: the pause that a block takes which gave up)
 }
 
 }  // namespace

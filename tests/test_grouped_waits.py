@@ -27,3 +27,16 @@ def test_the_two_warps_vote_on_every_wait_between_their_barriers():
     waits = re.findall(r"[^\n]*\bmbar_await\(|[^\n]*\bduo_await\(", loop)
     assert waits and all("duo_await(" in w for w in waits), waits
     assert "break" not in loop[loop.index("for (int st = half"):loop.index("if (++acc == 2)")]
+
+
+def test_a_block_that_gave_up_outlives_its_copies():
+    """Bulk loads (and partial sums of a cluster) that are under way when a wait gives up land in shared memory that the
+    block still owns: after its last barrier it waits a bounded time for them.  Nothing else follows that barrier but
+    the release of tensor memory."""
+    text = source("grouped.cu")
+    end = text[text.rindex("else cta_sync();"):text.index("cudaError_t launch_build")]
+    assert "settle_copies(abort_flag)" in end
+    helper = source("device.cuh")
+    body = helper[helper.index("void settle_copies("):]
+    body = body[:body.index("\n}")]
+    assert "globaltimer_ns()" in body and "kSettleNs" in body, body
