@@ -20,7 +20,7 @@ def assert_close(got, want, mags, what):
     assert bool(((got.double() - want).abs() <= want.abs() * 2.0 ** -8 + mags * 2e-6).all()), what
 
 
-@pytest.mark.parametrize("x_codes,w_codes,g_codes", itertools.product((False, True), repeat=3))
+@pytest.mark.parametrize("x_codes,w_codes,g_codes", list(itertools.product((False, True), repeat=3)))
 def test_backward_multiplies_by_the_codes_of_the_forward(x_codes, w_codes, g_codes):
     counts, N, K = [20, 0, 43], 80, 112
     rows, E = sum(counts), len(counts)
