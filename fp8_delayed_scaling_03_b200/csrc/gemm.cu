@@ -456,6 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
+      // Given up: the other CTA's loads were waited for here alone, so it has to
+      // know (settle_copies).
+      if (kPair && *abort_flag) st_cluster_u32(mapa_shared(smem_u32(const_cast<const int*>(abort_flag)), 1), 1u);
       // Whatever path led here (a bounded wait may have given up), no MMA may
       // still read shared memory or TMEM when the CTAs tear down.
       if constexpr (kPair) umma_commit_pair(smem_u32(drain));
@@ -708,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   if constexpr (kPair || kSplit) cluster_sync();  // no CTA leaves while another still signals or reads it
   else cta_sync();
+  if (threadIdx.x == 0) settle_copies(abort_flag);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
