@@ -148,9 +148,10 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits) {
 //   2-byte inputs: 127 v and the remainder r = 127 v - m top are exact in
 //     fp32, so |r| against top / 2 tells, and a tie goes to the even code.
 //     Ties are common there (bf16 values and amax have 8 significant bits):
-//     one in some 200, so every element is corrected, without a branch (a
-//     branch an element took a third longer).  The comparison adds m's lowest
-//     bit to r's pattern: above top / 2, or equal to it and m odd.
+//     one in 225 to 460 (rows of 11008 to 1024 normal values), so every
+//     element is corrected, without a branch (a branch an element took a third
+//     longer).  The comparison adds m's lowest bit to r's pattern: above
+//     top / 2, or equal to it and m odd.
 //   fp32 inputs: only where t is within 2e-5 of a border, 254 |v| is compared
 //     with (2 k + 1) top, which 64 bits hold exactly (one in some 25,000).
 template <typename T, bool kScaled>
