@@ -106,6 +106,10 @@ class Groups(ctypes.Structure):
                 ("stride_b", _I64), ("stride_d", _I64), ("scale_b_step", _I)]
 
 
+class GroupedPlanInfo(ctypes.Structure):
+    _fields_ = [("tile_lanes", _I), ("tile_cols", _I), ("split", _I), ("max_tiles", _I64)]
+
+
 class MmInt8Args(ctypes.Structure):
     _fields_ = [("m", _I64), ("n", _I64), ("k", _I64),
                 ("a", _P), ("lda", _I64), ("b", _P), ("ldb", _I64),
@@ -135,6 +139,8 @@ _SIGS = {
     "fp8_mm_pair": (_I, [ctypes.POINTER(MmArgs), ctypes.POINTER(MmArgs), _P]),
     "fp8_mm_batched": (_I, [ctypes.POINTER(MmArgs), _I64, _I64, _I64, _I64, _P]),
     "fp8_mm_grouped": (_I, [ctypes.POINTER(MmArgs), _I, ctypes.POINTER(Groups), _P]),
+    "fp8_mm_grouped_plan": (_I, [ctypes.POINTER(MmArgs), _I, ctypes.POINTER(Groups), _I, ctypes.POINTER(GroupedPlanInfo)]),
+    "fp8_mm_int8_plan": (_I, [ctypes.POINTER(MmInt8Args), _I, ctypes.POINTER(GroupedPlanInfo)]),
     "fp8_quantize_int8": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P]),
     "fp8_mm_int8": (_I, [ctypes.POINTER(MmInt8Args), _P]),
     "fp8_linear_grouped_forward": (_I, [ctypes.POINTER(LinearFwdArgs), ctypes.POINTER(Groups), _P]),
@@ -280,6 +286,21 @@ def fp8_mm_batched(a: MmArgs, batch: int, stride_a: int, stride_b: int, stride_d
 def fp8_mm_grouped(a: MmArgs, ragged: int, groups: Groups, device=None) -> None:
     """Products grouped by expert: FP8_RAGGED_M (rows of A and D) or FP8_RAGGED_K (the contraction)."""
     _check(_lib.fp8_mm_grouped(ctypes.byref(a), ragged, ctypes.byref(groups), _stream(device)), "fp8_mm_grouped")
+
+
+def fp8_mm_grouped_plan(a: MmArgs, ragged: int, groups: Groups, num_sms: int = 148) -> GroupedPlanInfo:
+    """The tiles fp8_mm_grouped would take on a GPU with num_sms SMs; host arithmetic only (no device needed)."""
+    info = GroupedPlanInfo()
+    _check(_lib.fp8_mm_grouped_plan(ctypes.byref(a), ragged, ctypes.byref(groups), num_sms, ctypes.byref(info)),
+           "fp8_mm_grouped_plan")
+    return info
+
+
+def fp8_mm_int8_plan(a: MmInt8Args, num_sms: int = 148) -> GroupedPlanInfo:
+    """The tiles fp8_mm_int8 would take on a GPU with num_sms SMs; host arithmetic only (no device needed)."""
+    info = GroupedPlanInfo()
+    _check(_lib.fp8_mm_int8_plan(ctypes.byref(a), num_sms, ctypes.byref(info)), "fp8_mm_int8_plan")
+    return info
 
 
 def fp8_quantize_int8(x: torch.Tensor, out: torch.Tensor, scale: torch.Tensor) -> None:

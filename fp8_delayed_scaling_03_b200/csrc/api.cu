@@ -971,6 +971,15 @@ bool grouped_live(const GroupedCall& c) {
   return c.groups > 0 && c.nlane > 0 && (c.ragged_k ? c.ncol > 0 : c.rows > 0);
 }
 
+void grouped_plan(const GroupedCall& c, int sms, fp8_grouped_plan_info* out) {
+  std::memset(out, 0, sizeof(*out));
+  if (!grouped_live(c)) return;
+  bool pair;
+  pick_grouped_tile(c, sms, &out->tile_cols, &pair, &out->split);
+  out->tile_lanes = pair ? 256 : 128;
+  out->max_tiles = grouped_max_tiles(c, out->tile_cols, out->tile_lanes);
+}
+
 int validate_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, int64_t ld_in, const int8_t* out,
                            int64_t ld_out, const float* scale) {
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return FP8_ERR_INVALID_ARG;
@@ -1458,6 +1467,26 @@ int fp8_mm_grouped(const fp8_mm_args* a, int ragged, const fp8_groups* g, fp8_st
   if ((s = grouped_call(*a, ragged, *g, &c))) return s;
   if (!grouped_live(c)) return FP8_OK;
   return run_grouped(c, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int fp8_mm_grouped_plan(const fp8_mm_args* a, int ragged, const fp8_groups* g, int num_sms,
+                        fp8_grouped_plan_info* out) {
+  if (!a || !out || num_sms <= 0) return FP8_ERR_INVALID_ARG;
+  int s = validate_groups(g);
+  if (s) return s;
+  GroupedCall c;
+  if ((s = grouped_call(*a, ragged, *g, &c))) return s;
+  grouped_plan(c, num_sms, out);
+  return FP8_OK;
+}
+
+int fp8_mm_int8_plan(const fp8_mm_int8_args* a, int num_sms, fp8_grouped_plan_info* out) {
+  if (!a || !out || num_sms <= 0) return FP8_ERR_INVALID_ARG;
+  GroupedCall c;
+  int s = int8_call(*a, &c);
+  if (s) return s;
+  grouped_plan(c, num_sms, out);
+  return FP8_OK;
 }
 
 int fp8_quantize_int8(const void* in, int in_dtype, int64_t rows, int64_t cols, int64_t ld_in, int8_t* out,

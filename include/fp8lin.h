@@ -335,6 +335,24 @@ typedef struct fp8_mm_int8_args {
 } fp8_mm_int8_args;
 FP8LIN_API int fp8_mm_int8(const fp8_mm_int8_args* args, fp8_stream_t stream);
 
+/* The tiles that fp8_mm_grouped or fp8_mm_int8 would take for these arguments
+ * on a GPU with num_sms SMs -- host arithmetic only, as fp8_mm_plan: nothing is
+ * launched and no operand or offset is read (the rule knows the number of
+ * groups, not their sizes).  The arguments are validated as the product
+ * validates them (same status codes).  Output (host pointer; all 0 where
+ * nothing would be launched):
+ *   tile_lanes  columns of D per tile: 128 on one CTA, 256 on a CTA pair
+ *   tile_cols   rows of D per tile: 16 .. 256
+ *   split       CTAs of a cluster that share each tile's contraction (1: none)
+ *   max_tiles   an upper bound on the launch's tiles */
+typedef struct {
+  int tile_lanes, tile_cols, split;
+  int64_t max_tiles;
+} fp8_grouped_plan_info;
+FP8LIN_API int fp8_mm_grouped_plan(const fp8_mm_args* args, int ragged, const fp8_groups* groups, int num_sms,
+                                   fp8_grouped_plan_info* out);
+FP8LIN_API int fp8_mm_int8_plan(const fp8_mm_int8_args* args, int num_sms, fp8_grouped_plan_info* out);
+
 /* Two independent GEMMs (the backward's dX and dW) in ONE launch over one
  * persistent tile schedule.  Same results as two fp8_mm calls; the tile
  * configuration (a->tile_cfg, or chosen for the pair when AUTO) and, for
