@@ -484,10 +484,15 @@ def linear_forward(x, w, ring_x: ScaleRing | None, ring_w: ScaleRing | None, bia
     xq = x.dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
     wq = w.dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
     y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if y is None else y
-    if x8 is None:
-        x8 = x.view(torch.uint8) if xq else fp8_alloc(M, K, dev)
-    if w8 is None:
-        w8 = w.view(torch.uint8) if wq else fp8_alloc(N, K, dev)
+    # codes are used in place: the result holds the operand itself, not a buffer that stays unwritten
+    if xq:
+        x8 = x.view(torch.uint8)
+    elif x8 is None:
+        x8 = fp8_alloc(M, K, dev)
+    if wq:
+        w8 = w.view(torch.uint8)
+    elif w8 is None:
+        w8 = fp8_alloc(N, K, dev)
     sc = torch.empty(4, dtype=torch.float32, device=dev) if scales is None else scales
     H = ring_x.H if ring_x is not None else (ring_w.H if ring_w is not None else hist_len)
     bias_dtype = FP8_DT_BF16
@@ -526,8 +531,10 @@ def linear_backward(g, fwd: ForwardResult, ring_g: ScaleRing | None, fmt_g=FP8_E
     K = fwd.x8.shape[1]
     dev = g.device
     gq = g.dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
-    if g8 is None:
-        g8 = g.view(torch.uint8) if gq else fp8_alloc(M, N, dev)
+    if gq:
+        g8 = g.view(torch.uint8)
+    elif g8 is None:
+        g8 = fp8_alloc(M, N, dev)
     dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if (need_dx and dx is None) else dx
     dw = torch.empty((N, K), dtype=torch.bfloat16, device=dev) if (need_dw and dw is None) else dw
     dbias = torch.empty(N, dtype=torch.bfloat16, device=dev) if (need_dbias and dbias is None) else dbias
