@@ -471,6 +471,12 @@ class ForwardResult:
     amax_w: torch.Tensor
 
 
+def _fp32_scale(scale: torch.Tensor | None, what: str) -> None:
+    """The scale of an operand in fp8 codes, read as one fp32 word (a missing one is the library's to refuse)."""
+    if scale is not None and (scale.dtype != torch.float32 or scale.numel() < 1):
+        raise ValueError(f"{what}: expected an fp32 scale, got {scale.dtype} {tuple(scale.shape)}")
+
+
 def linear_forward(x, w, ring_x: ScaleRing | None, ring_w: ScaleRing | None, bias=None, bias_scale=None,
                    fmt_x=FP8_E4M3, fmt_w=FP8_E4M3, x_scale_in=None, w_scale_in=None, hist_len=16,
                    y=None, x8=None, w8=None, scales=None) -> ForwardResult:
@@ -487,10 +493,12 @@ def linear_forward(x, w, ring_x: ScaleRing | None, ring_w: ScaleRing | None, bia
     # codes are used in place: the result holds the operand itself, not a buffer that stays unwritten
     if xq:
         x8 = x.view(torch.uint8)
+        _fp32_scale(x_scale_in, "x_scale_in")
     elif x8 is None:
         x8 = fp8_alloc(M, K, dev)
     if wq:
         w8 = w.view(torch.uint8)
+        _fp32_scale(w_scale_in, "w_scale_in")
     elif w8 is None:
         w8 = fp8_alloc(N, K, dev)
     sc = torch.empty(4, dtype=torch.float32, device=dev) if scales is None else scales
@@ -533,6 +541,7 @@ def linear_backward(g, fwd: ForwardResult, ring_g: ScaleRing | None, fmt_g=FP8_E
     gq = g.dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
     if gq:
         g8 = g.view(torch.uint8)
+        _fp32_scale(g_scale_in, "g_scale_in")
     elif g8 is None:
         g8 = fp8_alloc(M, N, dev)
     dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if (need_dx and dx is None) else dx

@@ -1,4 +1,5 @@
-"""Operands of linear_forward / linear_backward that come as fp8 codes: the codes that the results hold (on a GPU)."""
+"""Operands of linear_forward / linear_backward that come as fp8 codes: their scales, checked before any pointer is
+taken, and (on a GPU) the codes that the results hold."""
 import pytest
 import torch
 
@@ -7,6 +8,21 @@ import torch
 def fp8():
     import fp8_delayed_scaling_03_b200 as m
     return m
+
+
+def test_scales_of_codes_are_fp32(fp8):
+    """The kernels read a scale as one fp32 word: another type would be read as another number, an empty tensor past
+    its end."""
+    x, w, g = (torch.zeros(s, dtype=torch.uint8) for s in ((4, 16), (32, 16), (4, 32)))
+    one = torch.ones(1)
+    fwd = fp8.ForwardResult(None, x, w, one, one, one, one)
+    for bad in (torch.ones(1, dtype=torch.float64), torch.ones(1, dtype=torch.bfloat16), torch.ones(0)):
+        with pytest.raises(ValueError, match="x_scale_in"):
+            fp8.linear_forward(x, w, None, None, x_scale_in=bad, w_scale_in=one)
+        with pytest.raises(ValueError, match="w_scale_in"):
+            fp8.linear_forward(x, w, None, None, x_scale_in=one, w_scale_in=bad)
+        with pytest.raises(ValueError, match="g_scale_in"):
+            fp8.linear_backward(g, fwd, None, g_scale_in=bad)
 
 
 @pytest.mark.gpu
