@@ -850,7 +850,8 @@ def grouped_linear_backward(g, fwd: ForwardResult, offsets, ring_g: ScaleRing | 
 
 def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None, scale: torch.Tensor | None = None):
     """Rows of x to int8 by their own largest magnitude; returns (codes [rows, cols], scale [rows] fp32).  A weight
-    [N, K] quantized so has one scale per output channel."""
+    [N, K] quantized so has one scale per output channel.  The row stride of out is a multiple of 16, and every row's
+    bytes up to the next multiple of 16 columns are written (0), so they have to be out's own."""
     rows, cols, ldx = _matrix(x, "x")
     x_dtype = _wide_dtype(x.dtype)
     dev = _one_device(x, out, scale)

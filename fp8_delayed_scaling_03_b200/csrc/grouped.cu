@@ -48,11 +48,12 @@
 //
 // Measured on a B200 (graph replay; `of measured`: the copy bandwidth 6.53 TB/s
 // and twice the cuBLAS bf16 burst rate, 3.34 PFLOP/s):
-//   8192 rows in 8 equal groups, 11008 x 4096: forward 257 us (2.88 PFLOP/s,
-//     0.86), dX 241 us (3.06, 0.92), dW 295 us (2.50, 0.75); one group 256, 242
-//     and 242 us.  Short of power these are bound by the loads' latency against
-//     192 KB of stages; run without a pause the card's 1 kW limit holds them at
-//     2.1-2.4 PFLOP/s, where twice cuBLAS bf16's sustained rate is 2.8.
+//   8192 rows in 8 equal groups, 11008 x 4096: forward 257-274 us (2.69-2.88
+//     PFLOP/s, 0.81-0.86), dX 241-256 us (2.89-3.06, 0.86-0.92), dW 295-304 us
+//     (2.43-2.50, 0.73-0.75); one group 256-267, 242-252 and 242-253 us.  Short
+//     of power these are bound by the loads' latency against 192 KB of stages;
+//     run without a pause the card's 1 kW limit holds them at 2.1-2.4 PFLOP/s,
+//     where twice cuBLAS bf16's sustained rate is 2.8.
 //     dW's 721 MB of output take 140 us at the 5.1 TB/s that the store path
 //     reaches, and share the memory with the loads.
 //   128 rows over 64 groups, 6912 x 1536: 91 us, 6.1 TB/s of weights (0.92).
@@ -60,8 +61,10 @@
 //     launch takes (offsets from L2 and their scan 0.8, first load 1.2, the
 //     store's way out 0.6).
 //   dW of one row over 22 groups, 10181 x 128: 14.8 us, 3.9 TB/s of output; 14
-//     rows over 18 groups, 8317 x 1814 (rows of odd pitch): 166 us, 3.3 TB/s.
-//   int8, 8192 x 11008 x 4096: 241 us (3.07 PFLOP/s): kind::i8 has fp8's rate.
+//     rows over 18 groups, 8317 x 1814 (rows of odd pitch): 156-166 us, 3.3-3.5
+//     TB/s.
+//   int8, 8192 x 11008 x 4096: 238-241 us (3.07-3.10 PFLOP/s): kind::i8 has
+//     fp8's rate; fp32 out 253-256 us.
 #include <algorithm>
 #include <atomic>
 

@@ -210,8 +210,8 @@ __device__ __forceinline__ uint4 codes(const Chunk<T>& c, const RowScale& s) {
 // 352 threads an SM: 4096 rows of 11008 took 43.7 us, 33.9 with 40), 64 for
 // fp32, whose chunks take 32 (48 and fewer spill).
 //
-// Measured on a B200, inputs larger than L2: 8192 x 4096 bf16 23.0 us (4.4 TB/s
-// of the 6.5 TB/s a copy reaches), fp32 28.8 us (5.8 TB/s).  bf16 is bound by
+// Measured on a B200, inputs larger than L2: 8192 x 4096 bf16 23.0-23.9 us (4.2
+// to 4.4 TB/s of the 6.5 TB/s a copy reaches), fp32 28.6-28.9 us (5.8).  bf16 is bound by
 // instructions: some 11 an element, most of them the exact tie rule.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads, sizeof(T) == 2 ? 3 : 2) quantize_int8_kernel(const Int8QuantizeParams p) {
